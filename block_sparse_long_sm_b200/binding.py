@@ -27,7 +27,9 @@ EXPORTED = ("sparse_prefill_workspace_bytes", "sparse_prefill_plan", "sparse_pre
             "sparse_prefill_stats", "sparse_prefill_status_string", "sparse_prefill_plan_static",
             "sparse_decode_scratch_bytes", "sparse_decode_prepare", "sparse_decode_attn",
             "sparse_fp8_scales_floats", "sparse_fp8_scratch_bytes", "sparse_fp8_quantize",
-            "sparse_prefill_attn_fp8", "sparse_key_mass")
+            "sparse_prefill_attn_fp8", "sparse_key_mass", "sparse_qk_norm_rope",
+            "sparse_paged_append", "sparse_paged_workspace_bytes", "sparse_paged_select",
+            "sparse_paged_attn", "sparse_paged_status")
 
 
 class SpaParams(ctypes.Structure):
@@ -52,6 +54,34 @@ class SpaStats(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_ if name != "reserved"}
+
+
+class SpaRows(ctypes.Structure):
+    """A view of bf16 rows of 128: address and element strides (``spa_rows``)."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class SpaRopeParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("tokens", ctypes.c_int32), ("heads_q", ctypes.c_int32),
+        ("heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("table_rows", ctypes.c_int32), ("eps", ctypes.c_float),
+    ]
+
+
+class SpaPagedParams(ctypes.Structure):
+    _fields_ = [
+        ("heads_q", ctypes.c_int32), ("heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+        ("pages_per_seq", ctypes.c_int32), ("seqs", ctypes.c_int32), ("tokens", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64), ("softmax_scale", ctypes.c_float),
+        ("sink_pages", ctypes.c_int32), ("local_pages", ctypes.c_int32),
+        ("top_pages", ctypes.c_int32), ("wait_limit_us", ctypes.c_uint32),
+        ("debug_flags", ctypes.c_uint32),
+    ]
 
 
 class SpaError(RuntimeError):
@@ -95,6 +125,22 @@ def _load():
     lib.sparse_prefill_attn_fp8.restype = ctypes.c_int
     lib.sparse_key_mass.argtypes = [P, vp, vp, vp, i32, vp, sz, vp, vp]
     lib.sparse_key_mass.restype = ctypes.c_int
+    R, G = ctypes.POINTER(SpaRopeParams), ctypes.POINTER(SpaPagedParams)
+    rows = ctypes.POINTER(SpaRows)
+    lib.sparse_qk_norm_rope.argtypes = [R, rows, rows, vp, vp, vp, vp, rows, rows, vp, vp]
+    lib.sparse_qk_norm_rope.restype = ctypes.c_int
+    lib.sparse_paged_append.argtypes = [G, R, rows, rows, rows, vp, vp, vp, vp, vp, vp, rows, vp,
+                                        vp, vp, vp, vp]
+    lib.sparse_paged_append.restype = ctypes.c_int
+    lib.sparse_paged_workspace_bytes.argtypes = [G]
+    lib.sparse_paged_workspace_bytes.restype = sz
+    lib.sparse_paged_select.argtypes = [G, rows, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.sparse_paged_select.restype = ctypes.c_int
+    lib.sparse_paged_attn.argtypes = [G, rows, vp, vp, vp, vp, vp, vp, vp, rows, vp, vp, sz, vp,
+                                      vp]
+    lib.sparse_paged_attn.restype = ctypes.c_int
+    lib.sparse_paged_status.argtypes = [vp, vp]
+    lib.sparse_paged_status.restype = ctypes.c_int
     lib.sparse_prefill_status_string.argtypes = [ctypes.c_int]
     lib.sparse_prefill_status_string.restype = ctypes.c_char_p
     return lib
@@ -240,6 +286,193 @@ def sparse_key_mass(params: SpaParams, q, k, lse, window: int, workspace, mass,
     wb = _nbytes(workspace) if workspace_bytes is None else int(workspace_bytes)
     return int(_lib.sparse_key_mass(ctypes.byref(params), _ptr(q), _ptr(k), _ptr(lse), int(window),
                                     _ptr(workspace), wb, _ptr(mass), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the serving step around a paged cache
+# ---------------------------------------------------------------------------
+def make_rope_params(batch: int, tokens: int, heads_q: int, heads_kv: int, *, table_rows: int,
+                     rotary_dim: int = 128, interleaved: int = 0, eps: float = 1e-6,
+                     head_dim: int = 128) -> SpaRopeParams:
+    return SpaRopeParams(batch, tokens, heads_q, heads_kv, head_dim, rotary_dim,
+                         int(interleaved), int(table_rows), float(eps))
+
+
+def make_paged_params(heads_q: int, heads_kv: int, *, page_size: int, num_pages: int, seqs: int,
+                      tokens: int, pages_per_seq: int, page_stride: int = 0,
+                      softmax_scale: float = 0.0, sink_pages: int = 0, local_pages: int = 1,
+                      top_pages: int = 0, wait_limit_us: int = 0, debug_flags: int = 0,
+                      head_dim: int = 128) -> SpaPagedParams:
+    return SpaPagedParams(heads_q, heads_kv, head_dim, page_size, num_pages, pages_per_seq, seqs,
+                          tokens, int(page_stride), float(softmax_scale), sink_pages, local_pages,
+                          top_pages, int(wait_limit_us), int(debug_flags))
+
+
+def _rows(x, shape, name):
+    """A bf16 tensor [batch, tokens, heads, 128] or [tokens, heads, 128] (any strides but the
+    last dimension's), or an SpaRows, as a pointer to spa_rows."""
+    if x is None:
+        return None
+    if not isinstance(x, SpaRows):
+        if tuple(x.shape) != shape and (shape[0] != 1 or tuple(x.shape) != shape[1:]):
+            raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted {shape}")
+        if x.element_size() != 2 or not x.is_floating_point() or str(x.dtype) != "torch.bfloat16":
+            raise TypeError(f"{name}: {x.dtype}, wanted torch.bfloat16")
+        st = x.stride()
+        if st[-1] != 1 and x.numel():
+            raise ValueError(f"{name}: the 128 elements of a row have to be contiguous")
+        x = SpaRows(x.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+    return ctypes.byref(x)
+
+
+def _flat(x, dtype, count, name):
+    """Address of a contiguous tensor of at least ``count`` elements (raw addresses pass)."""
+    if x is None or isinstance(x, int):
+        return x
+    if str(x.dtype) not in dtype:
+        raise TypeError(f"{name}: {x.dtype}, wanted {dtype[0]}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: has to be contiguous")
+    if x.numel() < count:
+        raise ValueError(f"{name}: {x.numel()} elements, wanted {count}")
+    return x.data_ptr()
+
+
+_I32 = ("torch.int32",)
+_U32 = ("torch.int32", "torch.uint32")
+_F32 = ("torch.float32",)
+_BF16 = ("torch.bfloat16",)
+
+
+class _On:
+    """The device of a call's tensors made current, and the stream to use there."""
+
+    def __init__(self, stream, *tensors):
+        import torch
+        dev = None
+        for x in tensors:
+            if x is None or isinstance(x, (int, SpaRows)):
+                continue
+            d = x.device
+            if d.type != "cuda":
+                raise ValueError(f"a tensor on {d}: device memory is wanted")
+            if dev is not None and d != dev:
+                raise ValueError(f"tensors on {dev} and {d}")
+            dev = d
+        self.guard = None
+        if dev is not None and dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(dev)
+        self.given = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.given)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _cache(p: SpaPagedParams, x, name):
+    """Address of a K or V cache [num_pages, heads_kv, page_size, 128]."""
+    if x is None or isinstance(x, int):
+        return x
+    want = (p.num_pages, p.heads_kv, p.page_size, 128)
+    if tuple(x.shape) != want:
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted {want}")
+    if str(x.dtype) not in _BF16:
+        raise TypeError(f"{name}: {x.dtype}, wanted torch.bfloat16")
+    pitch = p.page_stride or p.heads_kv * p.page_size * 128
+    if x.stride()[1:] != (p.page_size * 128, 128, 1) or (x.shape[0] > 1 and x.stride(0) != pitch):
+        raise ValueError(f"{name}: strides {x.stride()} (pages {pitch} elements apart are wanted)")
+    return x.data_ptr()
+
+
+def sparse_qk_norm_rope(params: SpaRopeParams, q, k, q_weight, k_weight, positions, table, q_out,
+                        k_out, error, stream=None) -> int:
+    """Per-head RMS norm and position rotation of q and k; rows [batch, tokens, heads, 128]."""
+    r = params
+    with _On(stream, q, k, q_out, k_out, table, positions, error) as s:
+        sq, sk = (r.batch, r.tokens, r.heads_q, 128), (r.batch, r.tokens, r.heads_kv, 128)
+        return int(_lib.sparse_qk_norm_rope(
+            ctypes.byref(r), _rows(q, sq, "q"), _rows(k, sk, "k"),
+            _flat(q_weight, _BF16, 128, "q_weight"), _flat(k_weight, _BF16, 128, "k_weight"),
+            _flat(positions, _I32, r.batch * r.tokens, "positions"),
+            _flat(table, _F32, r.table_rows * r.rotary_dim, "table"), _rows(q_out, sq, "q_out"),
+            _rows(k_out, sk, "k_out"), _flat(error, _U32, 1, "error"), s))
+
+
+def _seq_args(p: SpaPagedParams, cu_q, kv_lens, block_table):
+    return (_flat(cu_q, _I32, p.seqs + 1, "cu_q"), _flat(kv_lens, _I32, p.seqs, "kv_lens"),
+            _flat(block_table, _I32, p.seqs * p.pages_per_seq, "block_table"))
+
+
+def sparse_paged_append(params: SpaPagedParams, rope: Optional[SpaRopeParams], q, k, v, q_weight,
+                        k_weight, table, cu_q, kv_lens, block_table, q_out, k_cache, v_cache,
+                        summary, error, stream=None) -> int:
+    """New tokens' k (normed, rotated) and v into the pages; q alike into q_out; summaries."""
+    p = params
+    with _On(stream, q, k, v, q_out, k_cache, v_cache, summary, cu_q, kv_lens, block_table, table,
+             error) as s:
+        sq, sk = (1, p.tokens, p.heads_q, 128), (1, p.tokens, p.heads_kv, 128)
+        return int(_lib.sparse_paged_append(
+            ctypes.byref(p), None if rope is None else ctypes.byref(rope), _rows(q, sq, "q"),
+            _rows(k, sk, "k"), _rows(v, sk, "v"), _flat(q_weight, _BF16, 128, "q_weight"),
+            _flat(k_weight, _BF16, 128, "k_weight"),
+            _flat(table, _F32, 0 if rope is None else rope.table_rows * rope.rotary_dim, "table"),
+            *_seq_args(p, cu_q, kv_lens, block_table), _rows(q_out, sq, "q_out"),
+            _cache(p, k_cache, "k_cache"), _cache(p, v_cache, "v_cache"),
+            _flat(summary, _BF16, p.num_pages * p.heads_kv * 256, "summary"),
+            _flat(error, _U32, 1, "error"), s))
+
+
+def sparse_paged_workspace_bytes(params: SpaPagedParams) -> int:
+    return int(_lib.sparse_paged_workspace_bytes(ctypes.byref(params)))
+
+
+def _list_width(p: SpaPagedParams) -> int:
+    return p.sink_pages + p.local_pages + p.top_pages
+
+
+def sparse_paged_select(params: SpaPagedParams, q, summary, cu_q, kv_lens, block_table, lists,
+                        counts, workspace, error, workspace_bytes=None, stream=None) -> int:
+    """Pages of every new token and kv head: sink, recent, and the best by upper bound."""
+    p = params
+    wb = _nbytes(workspace) if workspace_bytes is None else int(workspace_bytes)
+    with _On(stream, q, summary, cu_q, kv_lens, block_table, lists, counts, workspace,
+             error) as s:
+        n = p.tokens * p.heads_kv
+        return int(_lib.sparse_paged_select(
+            ctypes.byref(p), _rows(q, (1, p.tokens, p.heads_q, 128), "q"),
+            _flat(summary, _BF16, p.num_pages * p.heads_kv * 256, "summary"),
+            *_seq_args(p, cu_q, kv_lens, block_table),
+            _flat(lists, _I32, n * _list_width(p), "lists"), _flat(counts, _I32, n, "counts"),
+            _ptr(workspace), wb, _flat(error, _U32, 1, "error"), s))
+
+
+def sparse_paged_attn(params: SpaPagedParams, q, k_cache, v_cache, cu_q, kv_lens, block_table,
+                      lists, counts, o, lse, workspace, error, workspace_bytes=None,
+                      stream=None) -> int:
+    """Causal attention of the new tokens over their pages (lists None), or the listed ones."""
+    p = params
+    wb = _nbytes(workspace) if workspace_bytes is None else int(workspace_bytes)
+    with _On(stream, q, k_cache, v_cache, cu_q, kv_lens, block_table, lists, counts, o, lse,
+             workspace, error) as s:
+        n, rows = p.tokens * p.heads_kv, (1, p.tokens, p.heads_q, 128)
+        return int(_lib.sparse_paged_attn(
+            ctypes.byref(p), _rows(q, rows, "q"), _cache(p, k_cache, "k_cache"),
+            _cache(p, v_cache, "v_cache"), *_seq_args(p, cu_q, kv_lens, block_table),
+            _flat(lists, _I32, n * _list_width(p), "lists"), _flat(counts, _I32, n, "counts"),
+            _rows(o, rows, "o"), _flat(lse, _F32, p.tokens * p.heads_q, "lse"), _ptr(workspace),
+            wb, _flat(error, _U32, 1, "error"), s))
+
+
+def sparse_paged_status(error, stream=None) -> int:
+    """Waits for the stream, reads and clears the error word."""
+    with _On(stream, error) as s:
+        return int(_lib.sparse_paged_status(_flat(error, _U32, 1, "error"), s))
 
 
 def sparse_prefill_status_string(status: int) -> str:

@@ -312,6 +312,165 @@ SPA_API spa_status sparse_key_mass(const spa_params* p, const void* q, const voi
                                    const float* lse, int32_t window, void* workspace,
                                    size_t workspace_bytes, float* mass, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving step around a paged key/value cache
+ *
+ * The calls below carry one attention layer from the rows of the fused
+ * projection to the attention output of every new token, with the keys and
+ * values of all sequences in fixed-size pages:
+ *
+ *   sparse_qk_norm_rope  RMS norm of every q and k head and the position
+ *                        rotation in one pass, from any row layout to any
+ *                        other (head-major for sparse_prefill_plan);
+ *   sparse_paged_append  the same on the new tokens' k (and q), k and v written
+ *                        into the pages, and the per-page key minima and
+ *                        maxima kept for the selection;
+ *   sparse_paged_select  per new token and kv head, the pages with the largest
+ *                        upper bound of a logit, beside the sink and the most
+ *                        recent pages;
+ *   sparse_paged_attn    causal attention of the new tokens over their pages,
+ *                        all of them or the selected ones.
+ *
+ * Sequences.  S sequences bring n_s = cu_q[s+1] - cu_q[s] new tokens each
+ * (rows cu_q[s] .. cu_q[s+1] of q, k, v, o; n_s may be 0, and rows outside
+ * [cu_q[0], cu_q[S]) are neither read nor written).  kv_lens[s] is the length
+ * of sequence s with its new tokens, so token i of it has position
+ * kv_lens[s] - n_s + i.  Position x lies in page block_table[s][x / page_size],
+ * row x % page_size.
+ *
+ * Cache.  k_cache, v_cache: bf16 [num_pages][heads_kv][page_size][128], pages
+ * page_stride elements apart (0: contiguous), so that K and V may be the two
+ * halves of one buffer.  Rows of a page that no sequence has filled, and pages
+ * that no table names, may hold anything (NaN included).  The rows that a
+ * sequence has filled have to be finite.
+ *
+ * Rows.  A spa_rows views bf16 rows of 128 consecutive elements: row (b, t, h)
+ * starts at data + b * stride_batch + t * stride_token + h * stride_head
+ * (elements, multiples of 8; data 16-byte aligned).  In the paged calls
+ * stride_batch is not used.
+ *
+ * Errors.  error_word is a device uint32 (required, 4-byte aligned) that the
+ * caller clears once: bit0 is set when a bounded wait expires, bit1 when a
+ * device value is out of range -- cu_q that falls or passes the rows, a length
+ * below 0 or beyond pages_per_seq pages, a table entry outside the cache, a
+ * position outside the rotation table, a list entry that is not ascending or
+ * not visible.  A call never reads or writes out of bounds for such values:
+ * the sequence, page or row is left out and the outputs it reaches are
+ * undefined.  sparse_paged_status reads the word back.
+ *
+ * All pointers but the structs and the host arrays are device pointers of the
+ * current device, and the stream belongs to it.  Calls are asynchronous, keep
+ * nothing between calls and may be captured into a graph; calls that share a
+ * workspace must not overlap on the GPU. */
+typedef struct {
+  const void* data;      /* outputs are written through it as well */
+  int64_t stride_batch;
+  int64_t stride_token;
+  int64_t stride_head;
+} spa_rows;
+
+typedef struct {
+  int32_t batch;         /* >= 0 */
+  int32_t tokens;        /* rows per batch element, >= 0 */
+  int32_t heads_q;       /* >= 1 */
+  int32_t heads_kv;      /* >= 1 */
+  int32_t head_dim;      /* must be 128 */
+  int32_t rotary_dim;    /* 0 (no rotation), 16, 32, 64 or 128: dims [0, rotary_dim) rotate */
+  int32_t interleaved;   /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1) */
+  int32_t table_rows;    /* positions the table covers */
+  float eps;             /* >= 0, under the root of the norm */
+} spa_rope_params;
+
+typedef struct {
+  int32_t heads_q;       /* >= 1, a multiple of heads_kv; heads_q / heads_kv <= 128 */
+  int32_t heads_kv;      /* >= 1 */
+  int32_t head_dim;      /* must be 128 */
+  int32_t page_size;     /* 16, 32, 64 or 128 */
+  int32_t num_pages;     /* pages of the cache, >= 1 */
+  int32_t pages_per_seq; /* entries of a block_table row, >= 1 */
+  int32_t seqs;          /* S >= 0 */
+  int32_t tokens;        /* rows of q, k, v, o; cu_q[S] <= tokens */
+  int64_t page_stride;   /* elements between pages, a multiple of 128; 0: contiguous */
+  float softmax_scale;   /* > 0, or 0 for 1/sqrt(head_dim) */
+  int32_t sink_pages;    /* selection: first pages always kept, >= 0 */
+  int32_t local_pages;   /* selection: last visible pages always kept, >= 1 */
+  int32_t top_pages;     /* selection: best of the others, >= 0 */
+  uint32_t wait_limit_us;/* bound on every device-side wait; 0 -> 250,000 us */
+  uint32_t debug_flags;  /* 0 in normal use; SPA_DEBUG_STALL_ATTN */
+} spa_paged_params;
+
+/* y = x / sqrt(mean(x^2) + eps) * weight over the 128 elements of every q and k
+ * head row (weight bf16 [128]; NULL: no norm), then the rotation
+ *   y_i' = y_i c - y_j s,  y_j' = y_j c + y_i s
+ * of every pair (i, j) with (c, s) = (table[pos][m], table[pos][rotary_dim/2 + m])
+ * for pair m.  table: fp32 [table_rows][rotary_dim], cosines then sines, 16-byte
+ * aligned (any frequency scaling is the caller's).  pos = positions[b][t]
+ * (int32 [batch][tokens]; NULL: t).  Computed in fp32, rounded once to bf16.
+ * q or k may be NULL (with its output).  An output may be its own input (same
+ * strides); otherwise they must not overlap. */
+SPA_API spa_status sparse_qk_norm_rope(const spa_rope_params* r, const spa_rows* q,
+                                       const spa_rows* k, const void* q_weight,
+                                       const void* k_weight, const int32_t* positions,
+                                       const float* table, const spa_rows* q_out,
+                                       const spa_rows* k_out, uint32_t* error_word,
+                                       cudaStream_t stream);
+
+/* Writes k, normed and rotated at its position as by sparse_qk_norm_rope, and
+ * v as it is, into the pages.  r gives the norm and the rotation (batch 1,
+ * tokens and heads as in p); NULL: neither, and table and weights are unused.
+ * q / q_out: optional, the queries of the same tokens through the same norm
+ * (q_weight) and rotation; both NULL to leave them out.
+ * summary: optional, bf16 [num_pages][heads_kv][2][128]; the minimum and the
+ * maximum over the filled rows of every page that received a row are written
+ * (other pages' entries are left as they are).  Two sequences may not write to
+ * the same page in one call. */
+SPA_API spa_status sparse_paged_append(const spa_paged_params* p, const spa_rope_params* r,
+                                       const spa_rows* q, const spa_rows* k, const spa_rows* v,
+                                       const void* q_weight, const void* k_weight,
+                                       const float* table, const int32_t* cu_q,
+                                       const int32_t* kv_lens, const int32_t* block_table,
+                                       const spa_rows* q_out, void* k_cache, void* v_cache,
+                                       void* summary, uint32_t* error_word, cudaStream_t stream);
+
+/* Device workspace of sparse_paged_select and sparse_paged_attn (closed form;
+ * 0 when the params are invalid).  Needs no initialisation. */
+SPA_API size_t sparse_paged_workspace_bytes(const spa_paged_params* p);
+
+/* Pages of every new token t and kv head g.  With x the token's position, its
+ * visible pages are 0 .. x / page_size.  Kept are the first sink_pages, the
+ * last local_pages of them, and of the others the top_pages with the largest
+ *   u = max over q heads h of g, of sum_d max(q_hd min_d, q_hd max_d),
+ * an upper bound of q_h . k over the page's keys, from the page's summary.  The
+ * sum is taken in 64 bits and rounded once to fp32; ties go to the lowest page.
+ *   lists   int32 [tokens][heads_kv][sink + top + local pages], page numbers of
+ *           the sequence, ascending, then -1;
+ *   counts  int32 [tokens][heads_kv].
+ * A token of negative position has no pages.  The summaries of candidate pages
+ * have to be finite. */
+SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows* q,
+                                       const void* summary, const int32_t* cu_q,
+                                       const int32_t* kv_lens, const int32_t* block_table,
+                                       int32_t* lists, int32_t* counts, void* workspace,
+                                       size_t workspace_bytes, uint32_t* error_word,
+                                       cudaStream_t stream);
+
+/* Softmax attention of every new token over the keys at positions up to its
+ * own: all of them, or with lists and counts (as sparse_paged_select writes
+ * them, or the caller's own: ascending visible page numbers) those of the
+ * listed pages.  o: bf16 rows like q; lse: optional fp32 [tokens][heads_q]
+ * (natural log).  A token without keys gets o = 0, lse = -inf. */
+SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* q,
+                                     const void* k_cache, const void* v_cache,
+                                     const int32_t* cu_q, const int32_t* kv_lens,
+                                     const int32_t* block_table, const int32_t* lists,
+                                     const int32_t* counts, const spa_rows* o, float* lse,
+                                     void* workspace, size_t workspace_bytes,
+                                     uint32_t* error_word, cudaStream_t stream);
+
+/* Synchronises the stream, reads and clears the error word; SPA_ERR_TIMEOUT or
+ * SPA_ERR_INVALID when it was set. */
+SPA_API spa_status sparse_paged_status(uint32_t* error_word, cudaStream_t stream);
+
 /* Static string for a status code. */
 SPA_API const char* sparse_prefill_status_string(spa_status s);
 

@@ -32,11 +32,13 @@ Modules:
 * ``decode`` -- decode-shaped reuse of a prefill plan (SpotAttention Fig. 2,
   Sec. 3; KVpop Sec. 3, transposed attention);
 * ``fp8`` -- E4M3 rounding and SageAttention-style quantisation for an FP8
-  Computation Pass (SALE review, Summary).
+  Computation Pass (SALE review, Summary);
+* ``paged`` -- the serving step around a paged cache: norm and rotation of the
+  heads, page bounds and selection, attention of one query.
 
 Every function here is pinned by tests in ``tests/test_oracle_*.py`` against
 closed forms, invariants, special cases and brute force; see the module
 docstrings for which pin covers which function.
 """
 
-from . import attention, calibration, decode, fp8, selection  # noqa: F401
+from . import attention, calibration, decode, fp8, paged, selection  # noqa: F401

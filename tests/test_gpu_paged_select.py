@@ -1,0 +1,106 @@
+"""Page selection by upper bounds, and the attention over what it selects.
+
+The lists are whole numbers and have to be equal to the oracle's, whose scores are exact sums
+rounded once to fp32."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_long_sm_b200 as spa
+from oracle import paged as op
+from paged_common import D, Batch, attend, bits_of, check_attention, f64, to_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def run_select(b, sink, local, top, summary=None, ws=None):
+    p = b.params(sink_pages=sink, local_pages=local, top_pages=top)
+    sm = b.summary() if summary is None else summary
+    width = sink + local + top
+    lists = torch.full((b.T, b.hkv, width), -7, dtype=torch.int32, device="cuda")
+    counts = torch.full((b.T, b.hkv), -7, dtype=torch.int32, device="cuda")
+    ws = b.workspace(p) if ws is None else ws
+    spa.check(spa.sparse_paged_select(p, b.q, to_gpu(sm), b.cu_gpu, b.kv_gpu, b.table_gpu, lists,
+                                      counts, ws, b.error), "select")
+    return p, sm, lists, counts, ws
+
+
+def expected(b, sm, sink, local, top):
+    smf = f64(sm)
+    out = {}
+    for t, s, pos in b.tokens():
+        for g in range(b.hkv):
+            q = f64(b.qkv[t, g * b.group:(g + 1) * b.group])
+
+            def score(first, last):
+                ph = b.table[s, first:last]
+                return op.page_bounds(q, smf[ph, g, 0], smf[ph, g, 1])
+            out[(t, g)] = op.select_pages(pos, b.page, sink, local, top, score)
+    return out
+
+
+def check_lists(b, lists, counts, want):
+    lh, ch = lists.cpu().numpy(), counts.cpu().numpy()
+    rows = set()
+    for (t, g), pg in want.items():
+        rows.add(t)
+        assert ch[t, g] == pg.size, (t, g, ch[t, g], pg)
+        assert np.array_equal(lh[t, g, :pg.size], pg), (t, g, lh[t, g], pg)
+        assert np.all(lh[t, g, pg.size:] == -1)
+    for t in range(b.T):
+        if t not in rows:
+            assert np.all(lh[t] == -7) and np.all(ch[t] == -7)
+
+
+@pytest.mark.parametrize("hq,hkv,page,seqs,sink,local,top", [
+    (4, 2, 16, [(1, 700), (1, 33), (1, 1), (0, 20), (1, 0), (1, 160)], 1, 2, 5),
+    (8, 1, 16, [(3, 2100), (1, 1500)], 0, 1, 17),
+    (5, 1, 32, [(40, 900), (2, 2)], 2, 3, 4),
+    (20, 2, 64, [(1, 6000)], 1, 1, 30),
+    (2, 2, 128, [(1, 3000), (4, 130)], 0, 2, 1),
+    (3, 1, 16, [(1, 800)], 3, 4, 0),
+    (1, 1, 16, [(2, 5000)], 1, 1, 300),
+    (4, 4, 16, [(6, 3)], 1, 1, 1)])
+def test_select_and_attend(hq, hkv, page, seqs, sink, local, top):
+    b = Batch(hq, hkv, page, seqs, seed=hq * 7 + page, lead_rows=1, pad_rows=2)
+    p, sm, lists, counts, ws = run_select(b, sink, local, top)
+    want = expected(b, sm, sink, local, top)
+    check_lists(b, lists, counts, want)
+    o, lse = attend(b, p, lists, counts, ws=ws)
+    check_attention(b, o, lse, pages_of=lambda t, g: want[(t, g)])
+    b.ok()
+
+
+def test_ties_go_to_the_lowest_page():
+    b = Batch(4, 1, 16, [(1, 1600)], seed=1)
+    sm = b.summary()
+    for j in range(100):                       # three kinds of pages only
+        sm[b.table[0, j], 0, 0] = bits_of(np.full(D, -1.0 - j % 3))
+        sm[b.table[0, j], 0, 1] = bits_of(np.full(D, 1.0 + j % 3))
+    for top in (1, 20, 40, 70, 97):
+        p, _, lists, counts, _ = run_select(b, 1, 2, top, summary=sm)
+        check_lists(b, lists, counts, expected(b, sm, 1, 2, top))
+
+
+def test_signs_zeros_and_large_scores():
+    b = Batch(2, 1, 16, [(1, 3200)], seed=2)
+    rng = np.random.default_rng(0)
+    lo = rng.standard_normal((200, D)) * 10.0 ** rng.integers(-20, 15, size=(200, 1))
+    lo[::7] = 0.0
+    lo[3::7] = -0.0
+    hi = np.maximum(lo, rng.standard_normal((200, D)))
+    hi[::7] = 0.0
+    sm = b.summary()
+    sm[b.table[0, :200], 0, 0], sm[b.table[0, :200], 0, 1] = bits_of(lo), bits_of(hi)
+    for top in (3, 60, 150):
+        _, _, lists, counts, _ = run_select(b, 0, 1, top, summary=sm)
+        check_lists(b, lists, counts, expected(b, sm, 0, 1, top))
+
+
+def test_no_candidates_anywhere():
+    b = Batch(4, 2, 16, [(1, 30), (2, 16)], seed=3)
+    for sink, local, top in ((5, 5, 5), (0, 1, 0), (2, 1, 0)):
+        _, sm, lists, counts, _ = run_select(b, sink, local, top)
+        check_lists(b, lists, counts, expected(b, sm, sink, local, top))
+    b.ok()
