@@ -1,0 +1,177 @@
+"""Argument checks of the paged-cache calls: refused before any launch, on any machine."""
+
+import ctypes
+
+import pytest
+import torch
+
+import block_sparse_long_sm_b200 as spa
+from block_sparse_long_sm_b200 import binding
+
+A = 1 << 20            # an aligned stand-in address, never touched
+ROWS = spa.SpaRows(A, 0, 4096, 128)
+
+
+def paged(**kw):
+    base = dict(page_size=16, num_pages=8, seqs=2, tokens=4, pages_per_seq=4)
+    heads = (kw.pop("heads_q", 4), kw.pop("heads_kv", 2))
+    base.update(kw)
+    return spa.make_paged_params(*heads, **base)
+
+
+def attn(p, q=ROWS, k=A, v=A, cu=A, kv=A, table=A, lists=None, counts=None, o=ROWS, lse=A, ws=A,
+         nbytes=1 << 40, err=A):
+    return spa.sparse_paged_attn(p, q, k, v, cu, kv, table, lists, counts, o, lse, ws, err,
+                                 workspace_bytes=nbytes, stream=0)
+
+
+def select(p, q=ROWS, summary=A, lists=A, counts=A, ws=A, nbytes=1 << 40, err=A):
+    return spa.sparse_paged_select(p, q, summary, A, A, A, lists, counts, ws, err,
+                                   workspace_bytes=nbytes, stream=0)
+
+
+def append(p, r=None, q=None, k=ROWS, v=ROWS, qw=None, kw=None, table=A, qo=None, kc=A, vc=A,
+           sm=None, err=A, cu=A):
+    return spa.sparse_paged_append(p, r, q, k, v, qw, kw, table, cu, A, A, qo, kc, vc, sm, err,
+                                   stream=0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(head_dim=64), spa.SPA_ERR_UNSUPPORTED), (dict(page_size=8), spa.SPA_ERR_UNSUPPORTED),
+    (dict(page_size=48), spa.SPA_ERR_UNSUPPORTED), (dict(page_size=256), spa.SPA_ERR_UNSUPPORTED),
+    (dict(page_size=0), spa.SPA_ERR_INVALID), (dict(num_pages=0), spa.SPA_ERR_INVALID),
+    (dict(pages_per_seq=0), spa.SPA_ERR_INVALID), (dict(seqs=-1), spa.SPA_ERR_INVALID),
+    (dict(tokens=-1), spa.SPA_ERR_INVALID), (dict(heads_q=3), spa.SPA_ERR_INVALID),
+    (dict(heads_q=0), spa.SPA_ERR_INVALID), (dict(heads_kv=0), spa.SPA_ERR_INVALID),
+    (dict(heads_q=258, heads_kv=2), spa.SPA_ERR_UNSUPPORTED),
+    (dict(page_stride=100), spa.SPA_ERR_INVALID), (dict(page_stride=2048), spa.SPA_ERR_INVALID),
+    (dict(page_stride=-128), spa.SPA_ERR_INVALID), (dict(softmax_scale=-1.0), spa.SPA_ERR_INVALID),
+    (dict(softmax_scale=float("nan")), spa.SPA_ERR_INVALID),
+    (dict(sink_pages=-1), spa.SPA_ERR_INVALID), (dict(local_pages=0), spa.SPA_ERR_INVALID),
+    (dict(top_pages=-1), spa.SPA_ERR_INVALID),
+    (dict(num_pages=1 << 27), spa.SPA_ERR_UNSUPPORTED),
+    (dict(pages_per_seq=1 << 27), spa.SPA_ERR_UNSUPPORTED),
+    (dict(top_pages=1 << 30), spa.SPA_ERR_UNSUPPORTED),
+    (dict(tokens=1 << 30), spa.SPA_ERR_UNSUPPORTED)])
+def test_params(kw, code):
+    p = paged(**kw)
+    assert spa.sparse_paged_workspace_bytes(p) == 0
+    assert attn(p) == select(p) == append(p) == code
+
+
+def test_workspace_is_closed_form_and_covers_its_parts():
+    n = spa.sparse_paged_workspace_bytes(paged())
+    assert n >= 2 * 148 * 256 * 130 * 4
+    m = spa.sparse_paged_workspace_bytes(paged(tokens=1000, pages_per_seq=4096))
+    assert m - n >= (1000 * 4096 - 4 * 4) * 2 * 4 - 256
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(ws=0), spa.SPA_ERR_INVALID), (dict(ws=A + 8), spa.SPA_ERR_INVALID),
+    (dict(nbytes=100), spa.SPA_ERR_WORKSPACE), (dict(err=0), spa.SPA_ERR_INVALID),
+    (dict(err=A + 2), spa.SPA_ERR_INVALID), (dict(q=None), spa.SPA_ERR_INVALID),
+    (dict(q=spa.SpaRows(A + 8, 0, 128, 128)), spa.SPA_ERR_INVALID),
+    (dict(q=spa.SpaRows(A, 0, 4, 128)), spa.SPA_ERR_INVALID),
+    (dict(q=spa.SpaRows(A, 0, 128, 130)), spa.SPA_ERR_INVALID),
+    (dict(q=spa.SpaRows(A, 0, -128, 128)), spa.SPA_ERR_UNSUPPORTED)])
+def test_attn_and_select_arguments(kw, code):
+    assert attn(paged(), **kw) == code
+    if code != spa.SPA_ERR_UNSUPPORTED:
+        assert select(paged(), **kw) == code
+
+
+@pytest.mark.parametrize("kw", [dict(k=0), dict(v=A + 4), dict(cu=0), dict(kv=A + 1), dict(table=0),
+                                dict(o=None), dict(lse=A + 2), dict(lists=A), dict(counts=A),
+                                dict(lists=A + 1, counts=A)])
+def test_attn_arguments(kw):
+    assert attn(paged(), **kw) == spa.SPA_ERR_INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(summary=0), dict(summary=A + 8), dict(lists=0), dict(counts=0)])
+def test_select_arguments(kw):
+    assert select(paged(), **kw) == spa.SPA_ERR_INVALID
+
+
+def rope(**kw):
+    base = dict(table_rows=64)
+    base.update(kw)
+    dims = [base.pop(n, d) for n, d in (("batch", 1), ("tokens", 4), ("heads_q", 4), ("heads_kv", 2))]
+    return spa.make_rope_params(*dims, **base)
+
+
+@pytest.mark.parametrize("kw", [dict(k=None), dict(v=None), dict(kc=0), dict(vc=A + 8), dict(err=0),
+                                dict(cu=0), dict(q=ROWS), dict(qo=ROWS), dict(sm=A + 2),
+                                dict(r=rope(batch=2)), dict(r=rope(tokens=5)),
+                                dict(r=rope(heads_q=2)), dict(r=rope(), table=0),
+                                dict(r=rope(), kw=A + 2), dict(r=rope(eps=-1.0)),
+                                dict(k=spa.SpaRows(A, 0, 129, 128))])
+def test_append_arguments(kw):
+    assert append(paged(), **kw) == spa.SPA_ERR_INVALID
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(head_dim=64), spa.SPA_ERR_UNSUPPORTED), (dict(rotary_dim=96), spa.SPA_ERR_UNSUPPORTED),
+    (dict(rotary_dim=-2), spa.SPA_ERR_INVALID), (dict(rotary_dim=256), spa.SPA_ERR_INVALID),
+    (dict(interleaved=2), spa.SPA_ERR_INVALID), (dict(table_rows=0), spa.SPA_ERR_INVALID),
+    (dict(eps=float("inf")), spa.SPA_ERR_INVALID), (dict(batch=-1), spa.SPA_ERR_INVALID),
+    (dict(heads_q=0), spa.SPA_ERR_INVALID),
+    (dict(batch=1 << 16, tokens=1 << 16), spa.SPA_ERR_UNSUPPORTED)])
+def test_rope_params(kw, code):
+    r = rope(**kw)
+    assert spa.sparse_qk_norm_rope(r, ROWS, ROWS, None, None, None, A, ROWS, ROWS, A,
+                                   stream=0) == code
+
+
+def test_rope_arguments():
+    call = lambda q=ROWS, k=ROWS, qw=None, pos=None, table=A, qo=ROWS, ko=ROWS, err=A: \
+        spa.sparse_qk_norm_rope(rope(), q, k, qw, None, pos, table, qo, ko, err, stream=0)
+    for kw in (dict(q=None), dict(ko=None), dict(table=0), dict(table=A + 4), dict(err=0),
+               dict(pos=A + 2), dict(qw=A + 2), dict(q=spa.SpaRows(A, 1, 128, 128)),
+               dict(qo=spa.SpaRows(0, 0, 128, 128))):
+        assert call(**kw) == spa.SPA_ERR_INVALID, kw
+
+
+def test_empty_calls_launch_nothing():
+    assert attn(paged(tokens=0), q=None, o=None, k=0, v=0) == spa.SPA_OK
+    assert select(paged(seqs=0), q=None, summary=0) == spa.SPA_OK
+    assert append(paged(tokens=0), k=None, v=None) == spa.SPA_OK
+    assert spa.sparse_qk_norm_rope(rope(tokens=0), None, None, None, None, None, None, None, None, A,
+                                   stream=0) == spa.SPA_OK
+    assert spa.sparse_paged_status(0, stream=0) == spa.SPA_ERR_INVALID
+
+
+def test_tensor_checks_of_the_binding():
+    x = torch.zeros(4, 4, 128, dtype=torch.bfloat16)
+    rows = binding._rows(x, (1, 4, 4, 128), "q")._obj
+    assert (rows.stride_batch, rows.stride_token, rows.stride_head) == (0, 512, 128)
+    y = torch.zeros(2, 3, 5, 128, dtype=torch.bfloat16).transpose(1, 2)
+    rows = binding._rows(y, (2, 5, 3, 128), "q")._obj
+    assert (rows.stride_batch, rows.stride_token, rows.stride_head) == (1920, 128, 640)
+    for bad, exc in ((x.half(), TypeError), (x[:3], ValueError),
+                     (x.transpose(1, 2).contiguous().transpose(1, 2), ValueError)):
+        with pytest.raises(exc):
+            binding._rows(bad, (1, 4, 4, 128), "q")
+    p = paged()
+    cache = torch.zeros(8, 2, 16, 128, dtype=torch.bfloat16)
+    assert binding._cache(p, cache, "k") == cache.data_ptr()
+    for bad, exc in ((cache[:7], ValueError), (cache.float(), TypeError),
+                     (cache.transpose(1, 2).contiguous().transpose(1, 2), ValueError),
+                     (torch.zeros(8, 4, 16, 128, dtype=torch.bfloat16)[:, :2], ValueError)):
+        with pytest.raises(exc):
+            binding._cache(p, bad, "k")
+    both = torch.zeros(8, 4, 16, 128, dtype=torch.bfloat16)
+    assert binding._cache(paged(page_stride=4 * 16 * 128), both[:, 2:], "v") == both[:, 2:].data_ptr()
+    with pytest.raises(ValueError):
+        binding._flat(torch.zeros(3, dtype=torch.int32), binding._I32, 4, "cu_q")
+    with pytest.raises(TypeError):
+        binding._flat(torch.zeros(4, dtype=torch.int64), binding._I32, 4, "cu_q")
+    with pytest.raises(ValueError):
+        binding._flat(torch.zeros(4, 2, dtype=torch.int32)[:, 0], binding._I32, 4, "cu_q")
+    with pytest.raises(ValueError):                    # host memory
+        spa.sparse_paged_status(torch.zeros(1, dtype=torch.int32), stream=0)
+
+
+def test_struct_sizes_match_the_header():
+    assert ctypes.sizeof(spa.SpaRows) == 32
+    assert ctypes.sizeof(spa.SpaRopeParams) == 36
+    assert ctypes.sizeof(spa.SpaPagedParams) == 64
