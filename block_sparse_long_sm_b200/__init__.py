@@ -28,5 +28,7 @@ __all__ = list(_BINDING_NAMES)
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        return getattr(importlib.import_module(".binding", __name__), name)
+        value = getattr(importlib.import_module(".binding", __name__), name)
+        globals()[name] = value          # the next use does not come here again
+        return value
     raise AttributeError(name)

@@ -15,6 +15,11 @@ import math
 import os
 from typing import Optional
 
+try:                        # device memory and streams; raw addresses need neither
+    import torch as _torch
+except ImportError:  # pragma: no cover
+    _torch = None
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libspa.so")
 
@@ -176,11 +181,17 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+# the current stream's handle of a device; the public torch.cuda.current_stream() builds a
+# Stream object each time (3.2 us against 0.1 us a call)
+_raw_stream = getattr(getattr(_torch, "_C", None), "_cuda_getCurrentRawStream", None)
+
+
 def _stream(s) -> Optional[int]:
     if s is None:
         try:
-            import torch
-            return torch.cuda.current_stream().cuda_stream
+            if _raw_stream is not None:
+                return _raw_stream(_torch.cuda.current_device())
+            return _torch.cuda.current_stream().cuda_stream
         except Exception:  # pragma: no cover - no torch / no device
             return None
     if isinstance(s, int):
@@ -308,85 +319,97 @@ def make_paged_params(heads_q: int, heads_kv: int, *, page_size: int, num_pages:
                           top_pages, int(wait_limit_us), int(debug_flags))
 
 
-def _rows(x, shape, name):
-    """A bf16 tensor [batch, tokens, heads, 128] or [tokens, heads, 128] (any strides but the
-    last dimension's), or an SpaRows, as a pointer to spa_rows."""
+def _rows(x, batch, tokens, heads, name):
+    """A bf16 tensor [batch, tokens, heads, 128] or, for one batch element, [tokens, heads, 128]
+    (any strides but the last dimension's), or an SpaRows, as a reference to spa_rows."""
     if x is None:
         return None
-    if not isinstance(x, SpaRows):
-        if tuple(x.shape) != shape and (shape[0] != 1 or tuple(x.shape) != shape[1:]):
-            raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted {shape}")
-        if x.element_size() != 2 or not x.is_floating_point() or str(x.dtype) != "torch.bfloat16":
-            raise TypeError(f"{name}: {x.dtype}, wanted torch.bfloat16")
-        st = x.stride()
-        if st[-1] != 1 and x.numel():
-            raise ValueError(f"{name}: the 128 elements of a row have to be contiguous")
-        x = SpaRows(x.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
-    return ctypes.byref(x)
+    if x.__class__ is SpaRows:
+        return ctypes.byref(x)
+    sh, st = x.shape, x.stride()
+    if sh[-3:] != (tokens, heads, 128) or (sh[0] != batch if len(sh) == 4 else batch != 1) \
+            or not 3 <= len(sh) <= 4:
+        raise ValueError(f"{name}: shape {tuple(sh)}, wanted {(batch, tokens, heads, 128)}")
+    if x.dtype is not _torch.bfloat16:
+        raise TypeError(f"{name}: {x.dtype}, wanted torch.bfloat16")
+    if st[-1] != 1 and x.numel():
+        raise ValueError(f"{name}: the 128 elements of a row have to be contiguous")
+    return ctypes.byref(SpaRows(x.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2]))
 
 
 def _flat(x, dtype, count, name):
     """Address of a contiguous tensor of at least ``count`` elements (raw addresses pass)."""
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
-    if str(x.dtype) not in dtype:
-        raise TypeError(f"{name}: {x.dtype}, wanted {dtype[0]}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name}: has to be contiguous")
+    if x.dtype is not dtype:
+        raise TypeError(f"{name}: {x.dtype}, wanted {dtype}")
     if x.numel() < count:
         raise ValueError(f"{name}: {x.numel()} elements, wanted {count}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: has to be contiguous")
     return x.data_ptr()
 
 
-_I32 = ("torch.int32",)
-_U32 = ("torch.int32", "torch.uint32")
-_F32 = ("torch.float32",)
-_BF16 = ("torch.bfloat16",)
+def _i32(x, count, name):
+    return _flat(x, _torch.int32, count, name) if x.__class__ is not int else x
 
 
-class _On:
-    """The device of a call's tensors made current, and the stream to use there."""
+def _bf16(x, count, name):
+    return _flat(x, _torch.bfloat16, count, name) if x.__class__ is not int else x
 
-    def __init__(self, stream, *tensors):
-        import torch
-        dev = None
-        for x in tensors:
-            if x is None or isinstance(x, (int, SpaRows)):
-                continue
-            d = x.device
-            if d.type != "cuda":
-                raise ValueError(f"a tensor on {d}: device memory is wanted")
-            if dev is not None and d != dev:
-                raise ValueError(f"tensors on {dev} and {d}")
+
+def _f32(x, count, name):
+    return _flat(x, _torch.float32, count, name) if x.__class__ is not int else x
+
+
+def _word(x):
+    """Address of the error word: one int32 or uint32."""
+    if x is None or x.__class__ is int:
+        return x
+    return _flat(x, x.dtype if x.dtype is _torch.uint32 else _torch.int32, 1, "error")
+
+
+def _device(*tensors):
+    """The one CUDA device of the tensors given (None and raw addresses apart), or -1."""
+    dev = None
+    for x in tensors:
+        if x is None or x.__class__ is int or x.__class__ is SpaRows:
+            continue
+        d = x.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError("a tensor in host memory: device memory is wanted")
+            if dev is not None:
+                raise ValueError(f"tensors on devices {dev} and {d}")
             dev = d
-        self.guard = None
-        if dev is not None and dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(dev)
-        self.given = stream
+    return -1 if dev is None else dev
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.given)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device current, on the stream given or on that
+    device's current one."""
+    if dev < 0 or dev == _torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with _torch.cuda.device(dev):
+        return fn(*args, _stream(stream))
 
 
 def _cache(p: SpaPagedParams, x, name):
     """Address of a K or V cache [num_pages, heads_kv, page_size, 128]."""
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
-    want = (p.num_pages, p.heads_kv, p.page_size, 128)
-    if tuple(x.shape) != want:
-        raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted {want}")
-    if str(x.dtype) not in _BF16:
+    page, heads = p.page_size, p.heads_kv
+    if x.shape != (p.num_pages, heads, page, 128):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted "
+                         f"{(p.num_pages, heads, page, 128)}")
+    if x.dtype is not _torch.bfloat16:
         raise TypeError(f"{name}: {x.dtype}, wanted torch.bfloat16")
-    pitch = p.page_stride or p.heads_kv * p.page_size * 128
-    if x.stride()[1:] != (p.page_size * 128, 128, 1) or (x.shape[0] > 1 and x.stride(0) != pitch):
-        raise ValueError(f"{name}: strides {x.stride()} (pages {pitch} elements apart are wanted)")
+    pitch = p.page_stride or heads * page * 128
+    st = x.stride()
+    if st != (pitch, page * 128, 128, 1) and (
+            st[2:] != (128, 1) or (heads > 1 and st[1] != page * 128) or
+            (p.num_pages > 1 and st[0] != pitch)):
+        raise ValueError(f"{name}: strides {st} (pages {pitch} elements apart are wanted)")
     return x.data_ptr()
 
 
@@ -394,19 +417,14 @@ def sparse_qk_norm_rope(params: SpaRopeParams, q, k, q_weight, k_weight, positio
                         k_out, error, stream=None) -> int:
     """Per-head RMS norm and position rotation of q and k; rows [batch, tokens, heads, 128]."""
     r = params
-    with _On(stream, q, k, q_out, k_out, table, positions, error) as s:
-        sq, sk = (r.batch, r.tokens, r.heads_q, 128), (r.batch, r.tokens, r.heads_kv, 128)
-        return int(_lib.sparse_qk_norm_rope(
-            ctypes.byref(r), _rows(q, sq, "q"), _rows(k, sk, "k"),
-            _flat(q_weight, _BF16, 128, "q_weight"), _flat(k_weight, _BF16, 128, "k_weight"),
-            _flat(positions, _I32, r.batch * r.tokens, "positions"),
-            _flat(table, _F32, r.table_rows * r.rotary_dim, "table"), _rows(q_out, sq, "q_out"),
-            _rows(k_out, sk, "k_out"), _flat(error, _U32, 1, "error"), s))
-
-
-def _seq_args(p: SpaPagedParams, cu_q, kv_lens, block_table):
-    return (_flat(cu_q, _I32, p.seqs + 1, "cu_q"), _flat(kv_lens, _I32, p.seqs, "kv_lens"),
-            _flat(block_table, _I32, p.seqs * p.pages_per_seq, "block_table"))
+    b, t, hq, hk = r.batch, r.tokens, r.heads_q, r.heads_kv
+    dev = _device(q, k, q_weight, k_weight, positions, table, q_out, k_out, error)
+    return _call(
+        _lib.sparse_qk_norm_rope, dev, stream, ctypes.byref(r), _rows(q, b, t, hq, "q"),
+        _rows(k, b, t, hk, "k"), _bf16(q_weight, 128, "q_weight"),
+        _bf16(k_weight, 128, "k_weight"), _i32(positions, b * t, "positions"),
+        _f32(table, r.table_rows * r.rotary_dim, "table"), _rows(q_out, b, t, hq, "q_out"),
+        _rows(k_out, b, t, hk, "k_out"), _word(error))
 
 
 def sparse_paged_append(params: SpaPagedParams, rope: Optional[SpaRopeParams], q, k, v, q_weight,
@@ -414,18 +432,19 @@ def sparse_paged_append(params: SpaPagedParams, rope: Optional[SpaRopeParams], q
                         summary, error, stream=None) -> int:
     """New tokens' k (normed, rotated) and v into the pages; q alike into q_out; summaries."""
     p = params
-    with _On(stream, q, k, v, q_out, k_cache, v_cache, summary, cu_q, kv_lens, block_table, table,
-             error) as s:
-        sq, sk = (1, p.tokens, p.heads_q, 128), (1, p.tokens, p.heads_kv, 128)
-        return int(_lib.sparse_paged_append(
-            ctypes.byref(p), None if rope is None else ctypes.byref(rope), _rows(q, sq, "q"),
-            _rows(k, sk, "k"), _rows(v, sk, "v"), _flat(q_weight, _BF16, 128, "q_weight"),
-            _flat(k_weight, _BF16, 128, "k_weight"),
-            _flat(table, _F32, 0 if rope is None else rope.table_rows * rope.rotary_dim, "table"),
-            *_seq_args(p, cu_q, kv_lens, block_table), _rows(q_out, sq, "q_out"),
-            _cache(p, k_cache, "k_cache"), _cache(p, v_cache, "v_cache"),
-            _flat(summary, _BF16, p.num_pages * p.heads_kv * 256, "summary"),
-            _flat(error, _U32, 1, "error"), s))
+    t, hq, hk, seqs = p.tokens, p.heads_q, p.heads_kv, p.seqs
+    dev = _device(q, k, v, q_weight, k_weight, table, cu_q, kv_lens, block_table, q_out, k_cache,
+                  v_cache, summary, error)
+    return _call(
+        _lib.sparse_paged_append, dev, stream, ctypes.byref(p),
+        None if rope is None else ctypes.byref(rope), _rows(q, 1, t, hq, "q"),
+        _rows(k, 1, t, hk, "k"), _rows(v, 1, t, hk, "v"), _bf16(q_weight, 128, "q_weight"),
+        _bf16(k_weight, 128, "k_weight"),
+        _f32(table, 0 if rope is None else rope.table_rows * rope.rotary_dim, "table"),
+        _i32(cu_q, seqs + 1, "cu_q"), _i32(kv_lens, seqs, "kv_lens"),
+        _i32(block_table, seqs * p.pages_per_seq, "block_table"), _rows(q_out, 1, t, hq, "q_out"),
+        _cache(p, k_cache, "k_cache"), _cache(p, v_cache, "v_cache"),
+        _bf16(summary, p.num_pages * hk * 256, "summary"), _word(error))
 
 
 def sparse_paged_workspace_bytes(params: SpaPagedParams) -> int:
@@ -440,16 +459,15 @@ def sparse_paged_select(params: SpaPagedParams, q, summary, cu_q, kv_lens, block
                         counts, workspace, error, workspace_bytes=None, stream=None) -> int:
     """Pages of every new token and kv head: sink, recent, and the best by upper bound."""
     p = params
+    t, hk, seqs = p.tokens, p.heads_kv, p.seqs
+    dev = _device(q, summary, cu_q, kv_lens, block_table, lists, counts, workspace, error)
     wb = _nbytes(workspace) if workspace_bytes is None else int(workspace_bytes)
-    with _On(stream, q, summary, cu_q, kv_lens, block_table, lists, counts, workspace,
-             error) as s:
-        n = p.tokens * p.heads_kv
-        return int(_lib.sparse_paged_select(
-            ctypes.byref(p), _rows(q, (1, p.tokens, p.heads_q, 128), "q"),
-            _flat(summary, _BF16, p.num_pages * p.heads_kv * 256, "summary"),
-            *_seq_args(p, cu_q, kv_lens, block_table),
-            _flat(lists, _I32, n * _list_width(p), "lists"), _flat(counts, _I32, n, "counts"),
-            _ptr(workspace), wb, _flat(error, _U32, 1, "error"), s))
+    return _call(
+        _lib.sparse_paged_select, dev, stream, ctypes.byref(p), _rows(q, 1, t, p.heads_q, "q"),
+        _bf16(summary, p.num_pages * hk * 256, "summary"), _i32(cu_q, seqs + 1, "cu_q"),
+        _i32(kv_lens, seqs, "kv_lens"), _i32(block_table, seqs * p.pages_per_seq, "block_table"),
+        _i32(lists, t * hk * _list_width(p), "lists"), _i32(counts, t * hk, "counts"),
+        _ptr(workspace), wb, _word(error))
 
 
 def sparse_paged_attn(params: SpaPagedParams, q, k_cache, v_cache, cu_q, kv_lens, block_table,
@@ -457,22 +475,22 @@ def sparse_paged_attn(params: SpaPagedParams, q, k_cache, v_cache, cu_q, kv_lens
                       stream=None) -> int:
     """Causal attention of the new tokens over their pages (lists None), or the listed ones."""
     p = params
+    t, hq, hk, seqs = p.tokens, p.heads_q, p.heads_kv, p.seqs
+    dev = _device(q, k_cache, v_cache, cu_q, kv_lens, block_table, lists, counts, o, lse,
+                  workspace, error)
     wb = _nbytes(workspace) if workspace_bytes is None else int(workspace_bytes)
-    with _On(stream, q, k_cache, v_cache, cu_q, kv_lens, block_table, lists, counts, o, lse,
-             workspace, error) as s:
-        n, rows = p.tokens * p.heads_kv, (1, p.tokens, p.heads_q, 128)
-        return int(_lib.sparse_paged_attn(
-            ctypes.byref(p), _rows(q, rows, "q"), _cache(p, k_cache, "k_cache"),
-            _cache(p, v_cache, "v_cache"), *_seq_args(p, cu_q, kv_lens, block_table),
-            _flat(lists, _I32, n * _list_width(p), "lists"), _flat(counts, _I32, n, "counts"),
-            _rows(o, rows, "o"), _flat(lse, _F32, p.tokens * p.heads_q, "lse"), _ptr(workspace),
-            wb, _flat(error, _U32, 1, "error"), s))
+    return _call(
+        _lib.sparse_paged_attn, dev, stream, ctypes.byref(p), _rows(q, 1, t, hq, "q"),
+        _cache(p, k_cache, "k_cache"), _cache(p, v_cache, "v_cache"),
+        _i32(cu_q, seqs + 1, "cu_q"), _i32(kv_lens, seqs, "kv_lens"),
+        _i32(block_table, seqs * p.pages_per_seq, "block_table"),
+        _i32(lists, t * hk * _list_width(p), "lists"), _i32(counts, t * hk, "counts"),
+        _rows(o, 1, t, hq, "o"), _f32(lse, t * hq, "lse"), _ptr(workspace), wb, _word(error))
 
 
 def sparse_paged_status(error, stream=None) -> int:
     """Waits for the stream, reads and clears the error word."""
-    with _On(stream, error) as s:
-        return int(_lib.sparse_paged_status(_flat(error, _U32, 1, "error"), s))
+    return _call(_lib.sparse_paged_status, _device(error), stream, _word(error))
 
 
 def sparse_prefill_status_string(status: int) -> str:

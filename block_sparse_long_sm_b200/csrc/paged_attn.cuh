@@ -11,24 +11,26 @@
 // + head.  Keys come in tiles of 128, a tile being 128 / page_size whole pages
 // found through the block table, one TMA box per page and 64 columns.
 //
-// Two forms of one kernel, by how many rows a sequence brings:
-//   NT = 2  two row tiles (A: the first 128 / group tokens, B: the next) share
-//           every key tile; softmax warpgroup A / B works on its own rows.
-//   NT = 1  one row tile; the warpgroups take the key tiles in turn (even ones
-//           A, odd ones B), each with an accumulator of its own, and warpgroup
-//           A joins the two at the end.  A single token is bound by the
-//           bytes of K and V, and two independent chains of tiles hide the
-//           latency of one another's softmax.
+// Two ways through a segment, by the rows of its unit:
+//   two row tiles   (more than 128 / group tokens)  A: the first 128 / group
+//           tokens, B: the next; both read every key tile, softmax warpgroup
+//           A / B works on its own rows;
+//   one row tile    the warpgroups take the key tiles in turn (even ones A, odd
+//           ones B), each with an accumulator of its own, and warpgroup A
+//           joins the two at the end.  A single token is bound by the bytes of
+//           K and V, and two independent chains of tiles hide the latency of
+//           one another's softmax.
 // Either way step j of a segment (a run of key tiles) uses score slot,
 // accumulator and warpgroup j & 1, in the order
 //   S_0, S_1, PV_0, S_2, PV_1, S_3, PV_2, ...
 // so the tensor core has one product to do while the other slot's softmax runs.
+// A step batch that mixes prompt chunks and single tokens has both.
 //
-// Work split.  All (sequence, kv head, row tile) units lie end to end on one
-// line of key tiles, and each CTA (one per SM, persistent) takes an equal
-// piece of that line, found by a scan over the sequences' lengths: every SM
-// reads the same number of key tiles however ragged the batch is, one long
-// sequence included.  A unit that one CTA covers is finished there; the pieces
+// Work split.  All (sequence, kv head, row tiles) units lie end to end on one
+// line, a key tile being one step long (two with two row tiles: twice the
+// products), and each CTA (one per SM, persistent) takes an equal piece of
+// that line, found by a scan over the sequences' lengths: every SM has the same
+// work however ragged the batch is, one long sequence included.  A unit that one CTA covers is finished there; the pieces
 // of the others (at most two per CTA) go to the workspace in fp32 and
 // paged_combine_kernel joins them in the order of their CTAs, so that the
 // result does not depend on timing.
@@ -72,8 +74,8 @@ struct PagedRecord {
 // A CTA's share of one unit, handed by the walking warp to the others.
 struct PagedSeg {
   int tb, te;    // key tiles [tb, te) of the unit; te < 0: the piece is done
-  int nt;        // key tiles of the unit
-  int keys;      // keys it reads (0: none of its rows sees any)
+  int flags;     // kSeg*
+  int keys;      // keys the unit reads (0: none of its rows sees any)
   int tok0;      // first token row
   int ntok;      // tokens
   int pos0;      // position of the first
@@ -83,6 +85,9 @@ struct PagedSeg {
 };
 static_assert(sizeof(PagedSeg) == 48, "ring entries");
 constexpr int kPagedSegs = 4;
+constexpr int kSegDuo = 1;      // two row tiles
+constexpr int kSegStart = 2;    // holds the unit's first tile
+constexpr int kSegWhole = 4;    // holds all of them
 
 struct PagedAttnArgs {
   Seqs q;
@@ -97,15 +102,16 @@ struct PagedAttnArgs {
   int pitch;                 // 128-element rows between pages
   float sl2;                 // softmax scale * log2(e)
   PagedRecord* rec;          // [G]
-  float* part;               // [2 G] slots of rows * 130 floats
+  float* part;               // [2 G] slots of kPagedSlotFloats
   uint64_t wait_ns;
   uint32_t debug;
 };
 
-// Floats of one partial slot: O as [128 columns][rows], then m[rows], l[rows].
-__host__ __device__ constexpr long long paged_slot_floats(int rows) { return 130LL * rows; }
+// One partial slot: O [256 rows][128], m [256], l [256].
+constexpr int kPagedSlotRows = 256;
+constexpr long long kPagedSlotFloats = 130LL * kPagedSlotRows;
 
-// First CTA whose piece [total * c / G, total * (c + 1) / G) holds tile x.
+// The CTA whose piece [total * c / G, total * (c + 1) / G) holds point x.
 __device__ __forceinline__ int piece_of(long long x, long long total, int G) {
   return static_cast<int>(((x + 1) * G - 1) / total);
 }
@@ -113,7 +119,7 @@ __device__ __forceinline__ int piece_of(long long x, long long total, int G) {
 // ---------------------------------------------------------------------------
 // The units of a CTA's piece, in order.
 // ---------------------------------------------------------------------------
-template <int NT, bool LIST>
+template <bool LIST>
 struct PagedWalk {
   const PagedAttnArgs& a;
   long long x0, x1;          // the CTA's piece of the line
@@ -122,7 +128,8 @@ struct PagedWalk {
   int q0, n, pos_first;      // of the sequence
   int nr;                    // its row tiles
   // the current unit
-  int seq, tok0, ntok, pos0, keys, nt, flat;
+  int seq, tok0, ntok, pos0, keys, nt;
+  int w, flat;               // length of one of its tiles on the line, of all
 
   __device__ __forceinline__ explicit PagedWalk(const PagedAttnArgs& args) : a(args) {}
 
@@ -133,13 +140,20 @@ struct PagedWalk {
     return max(0, pos_first + min((r + 1) * tpt, n));
   }
 
-  // Key tiles of sequence s, one kv head.
-  __device__ __forceinline__ static long long head_tiles(const PagedAttnArgs& a, int s) {
+  // Length on the line of one tile of a unit of `tokens` tokens.
+  __device__ __forceinline__ static int tile_length(int tokens, int tpt1) {
+    return tokens > tpt1 ? 2 : 1;
+  }
+
+  // Length on the line of sequence s, one kv head.
+  __device__ __forceinline__ static long long head_length(const PagedAttnArgs& a, int s, bool& duo) {
     const Seq q = seq_at(a.q, s);
-    const int tpt = NT * a.tpt1;
-    long long w = 0;
-    for (int r = 0; r * tpt < q.n; ++r) w += tiles_of(tile_keys(q.kv - q.n, q.n, tpt, r));
-    return w;
+    const int tpt = 2 * a.tpt1;
+    long long len = 0;
+    for (int r = 0; r * tpt < q.n; ++r)
+      len += tiles_of(tile_keys(q.kv - q.n, q.n, tpt, r)) * tile_length(q.n - r * tpt, a.tpt1);
+    duo = q.n > a.tpt1;
+    return len;
   }
 
   __device__ __forceinline__ void load_seq() {
@@ -155,7 +169,7 @@ struct PagedWalk {
       q0 = q.q0;
       n = q.n;
       pos_first = q.kv - q.n;
-      nr = (n + NT * a.tpt1 - 1) / (NT * a.tpt1);
+      nr = (n + 2 * a.tpt1 - 1) / (2 * a.tpt1);
     }
   }
 
@@ -184,14 +198,16 @@ struct PagedWalk {
         }
       }
       nt = tiles_of(keys);
+      w = 1;
     } else {
-      const int tpt = NT * a.tpt1;
+      const int tpt = 2 * a.tpt1;
       tok0 = q0 + r * tpt;
       ntok = min(tpt, n - r * tpt);
       pos0 = pos_first + r * tpt;
       keys = tile_keys(pos_first, n, tpt, r);
       nt = tiles_of(keys);
-      flat = nt;
+      w = tile_length(ntok, a.tpt1);
+      flat = nt * w;
     }
   }
 
@@ -209,14 +225,16 @@ struct PagedWalk {
       s = s0;
       base = base0;
       load_seq();
-      const long long per_head = head_tiles(a, s);
+      bool duo;
+      const long long per_head = head_length(a, s, duo);
       g = static_cast<int>((x0 - base0) / per_head);
       base += g * per_head;
       r = 0;
       while (true) {
-        const int w = tiles_of(tile_keys(pos_first, n, NT * a.tpt1, r));
-        if (x0 < base + w || r + 1 >= nr) break;
-        base += w;
+        const int len = tiles_of(tile_keys(pos_first, n, 2 * a.tpt1, r)) *
+                        tile_length(n - 2 * r * a.tpt1, a.tpt1);
+        if (x0 < base + len || r + 1 >= nr) break;
+        base += len;
         ++r;
       }
     }
@@ -244,15 +262,16 @@ struct PagedWalk {
     set_unit();
   }
 
-  // The CTA's tiles [b, e) of the current unit; false: none of them exist.
+  // The CTA's tiles [b, e) of the current unit: those that begin on its piece;
+  // false: none of them exist.
   __device__ __forceinline__ bool range(int& b, int& e) const {
-    b = static_cast<int>(max(x0 - base, 0LL));
-    e = static_cast<int>(min(x1 - base, static_cast<long long>(nt)));
+    b = static_cast<int>((max(x0 - base, 0LL) + w - 1) / w);
+    e = static_cast<int>(min((x1 - base + w - 1) / w, static_cast<long long>(nt)));
     return b < e && ntok > 0;
   }
 };
 
-template <int NT, bool LIST>
+template <bool LIST>
 __global__ void __launch_bounds__(kPagedThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_k,
@@ -288,6 +307,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
   volatile float* ml = reinterpret_cast<volatile float*>(ctl + 1024);   // slot 1's m, l [128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine waits by itself
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPagedKStages; ++i) {
       mbar_init(bar_kfull(i), 1);
@@ -325,18 +345,31 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
   }
   // this CTA's piece of the line
   const int c = blockIdx.x;
-  // pieces: none is empty, so that every CTA between the first and the last of
-  // a shared unit has a part of it
+  // pieces: none without a tile of a unit that spans it, so that every CTA
+  // between the first and the last of a shared unit has a part of it
+  bool any_duo = false;
   auto pieces = [&](long long total) {
-    return static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1LL)));
+    return static_cast<int>(
+        min(static_cast<long long>(gridDim.x), max(total / (any_duo ? 2 : 1), 1LL)));
   };
   Found f{0, 0, 0, 0};
   if (LIST) {
     f.total = static_cast<long long>(a.q.T) * a.Hkv * a.wu;
   } else {
+    bool duo = false;
     f = block_find(
-        a.q.S, [&](int s) { return PagedWalk<NT, LIST>::head_tiles(a, s) * a.Hkv; },
-        [&](long long total) { return total * c / pieces(total); }, find);
+        a.q.S,
+        [&](int s) {
+          bool d;
+          const long long len = PagedWalk<LIST>::head_length(a, s, d) * a.Hkv;
+          duo |= d;
+          return len;
+        },
+        [&](long long total) {
+          any_duo = __syncthreads_or(duo);
+          return total * c / pieces(total);
+        },
+        find);
   }
   const int G = pieces(f.total);
   tc_fence_before();
@@ -360,35 +393,30 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       // ----------------------------------------------------------- loads
       const int ppt = 128 >> a.q.shift;             // pages per tile
       const uint32_t page_half = 128u * a.q.page;   // bytes of a page's 64 columns
-      int kt = 0, seg = 0;                          // key tiles, segments so far
+      int kt = 0, qu[2] = {0, 0}, qn = 0;           // key tiles, Q buffer uses, next buffer
       bool ok = true;
       PagedSeg sg;
       for (int i = 0; ok && take(i, sg); ++i) {
         if (sg.keys == 0) continue;
-        // Q
-        const int buf = NT == 1 ? seg & 1 : 0;
-        const int uses = NT == 1 ? seg >> 1 : seg;
-        if (uses > 0 && !(ok = warp_wait(bar_qfree(buf), (uses - 1) & 1, wc))) break;
-        if (NT == 1) {
-          if (lane == 0)
-            mbar_arrive_expect_tx(bar_qfull(buf), sg.ntok * a.group * 256u);
+        // Q: both buffers for two row tiles, else the buffers in turn
+        const bool duo = (sg.flags & kSegDuo) != 0;
+        const int first = duo ? 0 : qn, tiles = duo ? 2 : 1;
+        if (!duo) qn ^= 1;
+        for (int q = 0; ok && q < tiles; ++q) {
+          const int buf = first + q;
+          if (qu[buf] > 0 && !(ok = warp_wait(bar_qfree(buf), (qu[buf] - 1) & 1, wc))) break;
+          const int tok = sg.tok0 + q * a.tpt1;
+          const int n = min(a.tpt1, sg.ntok - q * a.tpt1);
+          if (lane == 0) mbar_arrive_expect_tx(bar_qfull(buf), n * a.group * 256u);
           __syncwarp();
-          for (int i = lane; i < sg.ntok; i += 32) {
-            const uint32_t at = s_q(buf) + i * a.group * 128u;
-            tma_load_3d(at, &tm_q, bar_qfull(buf), 0, sg.g * a.group, sg.tok0 + i);
-            tma_load_3d(at + kHalfBytes, &tm_q, bar_qfull(buf), 64, sg.g * a.group,
-                        sg.tok0 + i);
+          for (int k = lane; k < n; k += 32) {
+            const uint32_t at = s_q(buf) + k * a.group * 128u;
+            tma_load_3d(at, &tm_q, bar_qfull(buf), 0, sg.g * a.group, tok + k);
+            tma_load_3d(at + kHalfBytes, &tm_q, bar_qfull(buf), 64, sg.g * a.group, tok + k);
           }
-        } else if (lane == 0) {
-          const int tiles = sg.ntok > a.tpt1 ? 2 : 1;
-          mbar_arrive_expect_tx(bar_qfull(0), tiles * a.tpt1 * a.group * 256u);
-          for (int i = 0; i < tiles; ++i) {
-            tma_load_3d(s_q(i), &tm_q, bar_qfull(0), 0, sg.g * a.group,
-                        sg.tok0 + i * a.tpt1);
-            tma_load_3d(s_q(i) + kHalfBytes, &tm_q, bar_qfull(0), 64, sg.g * a.group,
-                        sg.tok0 + i * a.tpt1);
-          }
+          ++qu[buf];
         }
+        if (!ok) break;
         __syncwarp();
         // lane l < ppt: page l of the tile; its physical number is fetched one
         // tile ahead so that the table's latency overlaps the wait for a stage
@@ -441,7 +469,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           }
           __syncwarp();
         }
-        ++seg;
       }
       // no copy may be in flight when the CTA gives its shared memory back
       // (immediate in normal operation, bounded after an abort)
@@ -450,49 +477,53 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           mbar_drain(bar_kfull(i % kPagedKStages), (i / kPagedKStages) & 1, a.wait_ns);
         for (int i = max(0, kt - kPagedVStages); i < kt; ++i)
           mbar_drain(bar_vfull(i % kPagedVStages), (i / kPagedVStages) & 1, a.wait_ns);
-        for (int i = max(0, seg - (NT == 1 ? 2 : 1)); i < seg; ++i)
-          mbar_drain(bar_qfull(NT == 1 ? i & 1 : 0), (NT == 1 ? i >> 1 : i) & 1, a.wait_ns);
+        for (int i = 0; i < 2; ++i)
+          if (qu[i] > 0) mbar_drain(bar_qfull(i), (qu[i] - 1) & 1, a.wait_ns);
       }
     } else if (warp == 9) {
       // ------------------------------------------------------- MMA issuer
       bool ok = true;
       if (a.debug & 1u) ok = warp_wait(bar_stall, 0, wc);   // never signalled: test hook
-      int kt = 0, seg = 0, pc[2] = {0, 0}, oc[2] = {0, 0};
+      int kt = 0, qn = 0, qu[2] = {0, 0}, pc[2] = {0, 0}, oc[2] = {0, 0};
       PagedSeg sg;
       for (int i = 0; ok && take(i, sg); ++i) {
         if (sg.keys == 0) continue;
         if (lane == 0) {
-          const int tiles = sg.te - sg.tb, steps = NT == 2 ? 2 * tiles : tiles;
-          const int buf = NT == 1 ? seg & 1 : 0;
-          ok = mbar_wait(bar_qfull(buf), (NT == 1 ? seg >> 1 : seg) & 1, wc);
+          const int duo = (sg.flags & kSegDuo) ? 1 : 0;
+          const int tiles = sg.te - sg.tb, steps = tiles << duo;
+          const int buf = qn;
+          if (!duo) qn ^= 1;
           auto qk = [&](int j) -> bool {
-            const int h = j & 1, k = kt + (NT == 2 ? j >> 1 : j), st = k % kPagedKStages;
+            const int h = j & 1, k = kt + (j >> duo), st = k % kPagedKStages;
+            const int qb = duo ? h : buf;
+            if (j < 2 && (duo || j == 0)) {
+              if (!mbar_wait(bar_qfull(qb), qu[qb] & 1, wc)) return false;
+              ++qu[qb];
+            }
             if (!mbar_wait(bar_kfull(st), (k / kPagedKStages) & 1, wc)) return false;
             tc_fence_after();
-            const uint32_t qa = s_q(NT == 2 ? h : buf);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
               const uint32_t off = (ks >> 2) * kHalfBytes + (ks & 3) * 32u;
-              mma_bf16_ss(tmem + 128u * h, smem_desc_sw128(qa + off, 16),
+              mma_bf16_ss(tmem + 128u * h, smem_desc_sw128(s_q(qb) + off, 16),
                           smem_desc_sw128(s_k(st) + off, 16), kIdescQK, ks > 0 ? 1u : 0u);
             }
             mma_commit(bar_sfull(h));
-            if (NT == 1 || h == 1) mma_commit(bar_kempty(st));
-            if (j + 1 == steps) mma_commit(bar_qfree(buf));
+            if (!duo || h == 1) mma_commit(bar_kempty(st));
+            if (j + 1 + duo >= steps) mma_commit(bar_qfree(qb));
             return true;
           };
           auto pv = [&](int j) -> bool {
-            const int h = j & 1, k = kt + (NT == 2 ? j >> 1 : j), st = k % kPagedVStages;
+            const int h = j & 1, k = kt + (j >> duo), st = k % kPagedVStages;
             const bool first = j < 2;
             if (!mbar_wait(bar_pfull(h), pc[h] & 1, wc)) return false;
             ++pc[h];
             if (!mbar_wait(bar_vfull(st), (k / kPagedVStages) & 1, wc)) return false;
             if (!mbar_wait(bar_vclean(st), (k / kPagedVStages) & 1, wc)) return false;
-            if (first && (NT == 2 || j == 0)) {
-              // the previous segment's accumulators have been read
-              const int w = NT == 2 ? h : 0;
-              if (oc[w] > 0 && !mbar_wait(bar_ofree(w), (oc[w] - 1) & 1, wc)) return false;
-              ++oc[w];
+            if (first) {
+              // this accumulator of the segment before has been read
+              if (oc[h] > 0 && !mbar_wait(bar_ofree(h), (oc[h] - 1) & 1, wc)) return false;
+              ++oc[h];
             }
             tc_fence_after();
 #pragma unroll
@@ -501,8 +532,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                           smem_desc_sw128(s_v(st) + ks * 2048u, kHalfBytes), kIdescPV,
                           (!first || ks > 0) ? 1u : 0u);
             }
-            if (NT == 1 || h == 1) mma_commit(bar_vempty(st));
-            if (NT == 2 ? j + 2 >= steps : j + 1 == steps) mma_commit(bar_odone(NT == 2 ? h : 0));
+            if (!duo || h == 1) mma_commit(bar_vempty(st));
+            if (j + 2 >= steps) mma_commit(bar_odone(h));
             return true;
           };
           for (int j = 0; ok && j < 2 && j < steps; ++j) ok = qk(j);
@@ -511,7 +542,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (ok && j + 2 < steps) ok = qk(j + 2);
           }
           kt += tiles;
-          ++seg;
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
@@ -547,7 +577,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       }
     } else if (lane == 0) {
       // ----------------------------------------------- the CTA's segments
-      PagedWalk<NT, LIST> walk(a);
+      PagedWalk<LIST> walk(a);
       walk.x0 = f.total * c / G;
       walk.x1 = f.total * (c + 1) / G;
       PagedRecord mine{-1, 0, 0, 0};
@@ -566,12 +596,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           int tb, te;
           if (!walk.range(tb, te)) continue;
           if (tb == 0 && te < walk.nt) {            // other CTAs go on with it
-            mine.c1 = piece_of(walk.base + walk.nt - 1, f.total, G);
+            mine.c1 = piece_of(walk.base + static_cast<long long>(walk.w) * (walk.nt - 1), f.total, G);
             mine.g = walk.g;
             mine.tok0 = walk.tok0;
             mine.ntok = walk.ntok;
           }
-          hand(PagedSeg{tb, te, walk.nt, walk.keys, walk.tok0, walk.ntok, walk.pos0, walk.g,
+          const int flags = (walk.w == 2 ? kSegDuo : 0) | (tb == 0 ? kSegStart : 0) |
+                            (tb == 0 && te == walk.nt ? kSegWhole : 0);
+          hand(PagedSeg{tb, te, flags, walk.keys, walk.tok0, walk.ntok, walk.pos0, walk.g,
                         walk.seq, {0, 0, 0}});
         }
       }
@@ -588,19 +620,19 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     const int rt = row / a.group;                 // the row's token within a 128-row tile
     const int rh = row - rt * a.group;            // its q head within the group
     const bool row_fits = rt < a.tpt1;
-    constexpr int kRows = 128 * NT;
-    int sc = 0, oc = 0;
+    int sc = 0, oc[2] = {0, 0}, xc = 0;           // steps, accumulator uses, hand-overs
     bool ok = true;
     PagedSeg sg;
     for (int i = 0; ok && take(i, sg); ++i) {
       const int tb = sg.tb, te = sg.te;
-      const int ti = rt + (NT == 2 ? hd * a.tpt1 : 0);
+      const bool duo = (sg.flags & kSegDuo) != 0;
+      const int ti = rt + (duo ? hd * a.tpt1 : 0);
       const bool valid_row = row_fits && ti < sg.ntok;
       const long long tok = static_cast<long long>(sg.tok0) + ti;
       const int head = sg.g * a.group + rh;
       if (sg.keys == 0) {
         // no row of the unit sees a key
-        if (valid_row && (NT == 2 || hd == 0)) {
+        if (valid_row && (duo || hd == 0)) {
           uint4* dst = reinterpret_cast<uint4*>(a.o.at(0, tok, head));
           for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
           if (a.lse) a.lse[tok * a.Hq + head] = -INFINITY;
@@ -612,7 +644,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       const bool busy = __any_sync(0xffffffffu, valid_row);
       float m_used = -INFINITY, lsum = 0.f;
       bool started = false;
-      for (int t = NT == 2 ? tb : tb + hd; t < te; t += NT == 2 ? 1 : 2) {
+      for (int t = duo ? tb : tb + hd; t < te; t += duo ? 1 : 2) {
         if (!(ok = warp_wait(bar_sfull(hd), sc & 1, wc))) break;
         ++sc;
         tc_fence_after();
@@ -688,27 +720,29 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       }
       if (!ok) break;
       // ----------------------------------------------------- segment's end
-      const bool whole = tb == 0 && te == sg.nt;
-      const bool from_start = tb == 0;
-      const int oseg = oc++;
-      if (NT == 1 && hd == 1) {
+      const bool whole = (sg.flags & kSegWhole) != 0;
+      const bool two = !duo && te - tb > 1;       // both accumulators belong to these rows
+      const int use0 = oc[0]++, use1 = oc[1];
+      if (duo || two) ++oc[1];
+      if (!duo && hd == 1) {
+        if (!two) continue;
         // hand (m, l) to warpgroup 0, which joins the two accumulators; it has
-        // read the previous segment's once it has freed those accumulators
-        if (oseg > 0 && !(ok = warp_wait(bar_ofree(0), (oseg - 1) & 1, wc))) break;
+        // read the last pair once it has freed the second accumulator
+        if (use1 > 0 && !(ok = warp_wait(bar_ofree(1), (use1 - 1) & 1, wc))) break;
         ml[row] = m_used;
         ml[128 + row] = lsum;
         mbar_arrive(bar_xch);
+        if (!(ok = warp_wait(bar_odone(1), use1 & 1, wc))) break;
         continue;
       }
-      if (NT == 1 && !(ok = warp_wait(bar_xch, oseg & 1, wc))) break;
-      if (!(ok = warp_wait(bar_odone(NT == 2 ? hd : 0), oseg & 1, wc))) break;
+      if (two && !(ok = warp_wait(bar_xch, xc++ & 1, wc))) break;
+      if (!(ok = warp_wait(bar_odone(hd), (hd ? use1 : use0) & 1, wc))) break;
+      if (two && !(ok = warp_wait(bar_odone(1), use1 & 1, wc))) break;
       tc_fence_after();
-      const int slot = 2 * c + (from_start ? 1 : 0);
-      float* part = a.part + slot * paged_slot_floats(kRows);
-      const int prow = (NT == 2 ? hd * 128 : 0) + row;
-      // NT = 1: both slots' accumulators, weighted
+      float* part = a.part + (2LL * c + ((sg.flags & kSegStart) ? 1 : 0)) * kPagedSlotFloats;
+      const int prow = (duo ? hd * 128 : 0) + row;
       float fac0 = 1.f, fac1 = 0.f, m = m_used, l = lsum;
-      if (NT == 1) {
+      if (two) {
         const float m1 = ml[row];
         m = fmaxf(m_used, m1);
         const float base = m == -INFINITY ? 0.f : m;
@@ -716,31 +750,45 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         fac1 = fast_exp2(m1 - base);
         l = lsum * fac0 + ml[128 + row] * fac1;
       }
-      const bool two = NT == 1 && te - tb > 1;    // slot 1 has an accumulator
       const float inv = whole ? (l > 0.f ? 1.0f / l : 0.f) : 1.f;
+      fac0 *= inv;
+      fac1 *= inv;
       if (busy) {
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
-          uint32_t ov[32], ow[32];
+          uint32_t ov[32];
           tmem_ld32(tmem + lane_off + o_col + 32u * q, ov);
-          if (two) tmem_ld32(tmem + lane_off + 384u + 32u * q, ow);
           tmem_ld_wait();
-          float y[32];
+          // a row that sees no key has accumulated nothing but 0 * V
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float x = __uint_as_float(ov[e]);
-            if (NT == 1) x *= fac0;
-            if (two) x = fmaf(__uint_as_float(ow[e]), fac1, x);
-            // a row that sees no key has accumulated nothing but 0 * V
-            y[e] = l > 0.f ? x * inv : 0.f;
+          for (int e = 0; e < 32; ++e)
+            ov[e] = __float_as_uint(l > 0.f ? __uint_as_float(ov[e]) * fac0 : 0.f);
+          if (two) {
+            uint32_t ow[32];
+            tmem_ld32(tmem + lane_off + 384u + 32u * q, ow);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              ov[e] = __float_as_uint(
+                  l > 0.f ? fmaf(__uint_as_float(ow[e]), fac1, __uint_as_float(ov[e])) : 0.f);
           }
           if (valid_row) {
             if (whole) {
               uint4* dst = reinterpret_cast<uint4*>(a.o.at(0, tok, head) + 32 * q);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) dst[i] = pack8(y + 8 * i);
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t* x = ov + 8 * i;
+                dst[i] = make_uint4(
+                    pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                    pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                    pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                    pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
+              }
             } else {
+              uint4* dst = reinterpret_cast<uint4*>(part + prow * 128 + 32 * q);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) part[(32 * q + e) * kRows + prow] = y[e];
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
             }
           }
         }
@@ -750,13 +798,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
               a.lse[tok * a.Hq + head] =
                   l > 0.f ? m * 0.69314718055994531f + logf(l) : -INFINITY;
           } else {
-            part[128 * kRows + prow] = m;
-            part[129 * kRows + prow] = l;
+            part[128 * kPagedSlotRows + prow] = m;
+            part[129 * kPagedSlotRows + prow] = l;
           }
         }
       }
       tc_fence_before();
-      mbar_arrive(bar_ofree(NT == 2 ? hd : 0));
+      mbar_arrive(bar_ofree(hd));
+      if (two) mbar_arrive(bar_ofree(1));
     }
   }
 
@@ -766,45 +815,71 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of every unit that several CTAs share: block x looks at the
-// record of CTA x.  O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
-// A thread has one row and eight columns; eight rows (32 bytes of a partial's
-// column) by sixteen column groups per block and step.
-template <int NT>
-__global__ void __launch_bounds__(128) paged_combine_kernel(const PagedAttnArgs a) {
+// Joins the pieces of every unit that several CTAs share: blocks x look at the
+// record of CTA x.  O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.  A warp
+// per row: the lanes read the pieces' (m, l) side by side and turn them into
+// weights, then each lane sums four columns over the pieces, all loads
+// independent (a serial merge took 17 us for 8 pieces of one token).
+constexpr int kCombineThreads = 256;
+
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedAttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedRecord rec = a.rec[blockIdx.x];
   if (rec.c1 < 0) return;
-  constexpr int kRows = 128 * NT;
-  const int c0 = blockIdx.x;
-  const int col = 8 * (threadIdx.x >> 3);
-  for (int rb = 8 * blockIdx.y; rb < kRows; rb += 8 * gridDim.y) {
-    const int prow = rb + (threadIdx.x & 7);
-    const int row = prow & 127;
-    const int rt = row / a.group;
-    const int ti = rt + (prow >> 7) * a.tpt1;
-    if (rt >= a.tpt1 || ti >= rec.ntok) continue;
-    float m = -INFINITY, l = 0.f, y[8];
+  const int c0 = blockIdx.x, np = rec.c1 - c0 + 1;
+  const int lane = threadIdx.x & 31;
+  const int rows = rec.ntok * a.group;
+  const int stride = gridDim.y * (kCombineThreads / 32);
+  // slot of piece i: the first CTA's is its second
+  auto slot = [&](int i) {
+    return a.part + (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * kPagedSlotFloats;
+  };
+  for (int i = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5); i < rows; i += stride) {
+    const int ti = i / a.group, hh = i - ti * a.group;
+    const int tile = ti >= a.tpt1 ? 1 : 0;
+    const int prow = tile * 128 + (ti - tile * a.tpt1) * a.group + hh;
+    constexpr int kGroups = 5;                     // of 32 pieces: up to 160 CTAs
+    float mw[kGroups], lw[kGroups], m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = 0.f;
-    for (int c = c0; c <= rec.c1; ++c) {
-      const float* part = a.part + (2LL * c + (c == c0 ? 1 : 0)) * paged_slot_floats(kRows);
-      const float mc = part[128 * kRows + prow];
-      if (mc == -INFINITY) continue;
-      const float mn = fmaxf(m, mc);
-      const float fo = exp2f(m - mn), fn = exp2f(mc - mn);
-      l = l * fo + part[129 * kRows + prow] * fn;
+    for (int k = 0; k < kGroups; ++k) {
+      const int p = 32 * k + lane;
+      mw[k] = p < np ? slot(p)[128 * kPagedSlotRows + prow] : -INFINITY;
+      lw[k] = p < np ? slot(p)[129 * kPagedSlotRows + prow] : 0.f;
+      m = fmaxf(m, mw[k]);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * fo + part[(col + i) * kRows + prow] * fn;
-      m = mn;
+    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      mw[k] = mw[k] == -INFINITY ? 0.f : exp2f(mw[k] - m);
+      l = fmaf(lw[k], mw[k], l);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const int n = min(32, np - 32 * k);
+#pragma unroll 8
+      for (int p = 0; p < n; ++p) {
+        const float wgt = __shfl_sync(0xffffffffu, mw[k], p);
+        const float4 x =
+            *reinterpret_cast<const float4*>(slot(32 * k + p) + prow * 128 + 4 * lane);
+        acc.x = fmaf(x.x, wgt, acc.x);
+        acc.y = fmaf(x.y, wgt, acc.y);
+        acc.z = fmaf(x.z, wgt, acc.z);
+        acc.w = fmaf(x.w, wgt, acc.w);
+      }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] *= inv;
     const long long tok = static_cast<long long>(rec.tok0) + ti;
-    const int head = rec.g * a.group + (row - rt * a.group);
-    *reinterpret_cast<uint4*>(a.o.at(0, tok, head) + col) = pack8(y);
-    if (a.lse && col == 0)
+    const int head = rec.g * a.group + hh;
+    uint2 y;
+    y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(a.o.at(0, tok, head) + 4 * lane) = y;
+    if (a.lse && lane == 0)
       a.lse[tok * a.Hq + head] = l > 0.f ? m * 0.69314718055994531f + logf(l) : -INFINITY;
   }
 }

@@ -10,21 +10,34 @@
 // page that holds a large logit for any of them scores low.  512 bytes of
 // summary stand for 512 * page_size bytes of keys and values.
 //
-// Exactness.  Which pages are kept is a whole-number output, so the scores are
-// taken so that no order of summation can change them: a product of two bf16
-// is exact in fp32, a sum of 128 of them in 64 bits is off by at most 2^-46 of
-// the largest partial sum, and rounding that once to fp32 gives the same value
-// whatever the order (but for sums within 2^-46 of a rounding border).
+// The sum is two products, max(q, 0) . max + min(q, 0) . min, so it runs on
+// the tensor cores (mma.sync m16n8k16: sixteen rows of tokens x heads against
+// eight pages; the call is bound by the bytes of the summaries, 512 for 16 x
+// 512 multiply-adds, which this instruction's rate serves many times over).
 //
-// page_score_kernel    a thread quad per page: each lane reads four 16-byte
-//                      pieces of the minima and of the maxima (64 contiguous
-//                      bytes per quad and load), then serves the q heads from
-//                      shared memory.  max(q min, q max) is q times the
-//                      maximum where q >= 0 and times the minimum elsewhere.
-// page_top_kernel      one block per token and kv head: a radix search of the
-//                      score with rank top_pages (four passes of eight bits
-//                      over the order-preserving integer image), then one scan
-//                      that writes the kept pages in ascending order.
+// Exactness.  Which pages are kept is a whole-number output, defined by the
+// sum taken in 64 bits and rounded once to fp32.  The tensor core's fp32 sum
+// differs from it by at most
+//
+//     e = 2^-14 sum_d |q_d| max(|min_d|, |max_d|):
+//
+// the products of two bf16 are exact, and each of the 16 accumulating steps
+// adds 16 of them with an error of at most 17 * 2^-23 of the sum of
+// magnitudes, 2^-14.9 in all (the rounding to fp32 is 2^-24).  A third product
+// gives that sum of magnitudes for every page.  With t the score of rank
+// top_pages among the fp32 sums and e the largest bound of the token and head,
+// a page above t + 2e is among the best whatever the errors, one below t - 2e
+// is not, and only the pages between -- two or three of thousands -- are
+// summed again in 64 bits and ranked exactly.
+//
+// page_score_kernel  a warp per 32 pages.  All four lanes that share a page
+//                    read 16-byte pieces of it (the order of a dot product's
+//                    terms is free, so the pieces are the matrix operand as
+//                    they come).  Tokens of one sequence that fit into the
+//                    sixteen rows share the loads.
+// page_top_kernel    one block per token and kv head: radix search of the
+//                    score of rank top_pages, the exact sums between, and one
+//                    scan that writes the kept pages in ascending order.
 #pragma once
 
 #include "paged_seqs.cuh"
@@ -36,18 +49,20 @@ struct SelectArgs {
   Seqs q;
   Rows xq;
   const __nv_bfloat16* summary;   // [num_pages][Hkv][2][128]
-  float* score;                   // [T][Hkv][per_seq]
+  float2* score;                  // [T][Hkv][per_seq]: fp32 sum, sum of magnitudes
   int32_t* lists;                 // [T][Hkv][width]
   int32_t* counts;                // [T][Hkv]
   int Hkv, group;
   int sink, local, top, width;
   int chunks;                     // score blocks per (token, kv head)
+  int tm;                         // tokens that share the sixteen rows
 };
 
 constexpr int kScoreThreads = 128;
-constexpr int kScorePages = 64;          // pages per score block
-constexpr int kScoreHeads = 8;           // q heads per pass
+constexpr int kWarpPages = 32;           // pages per warp
+constexpr int kScorePages = kWarpPages * kScoreThreads / 32;
 constexpr int kTopThreads = 256;
+constexpr int kTopKeys = 8192;           // scores kept in shared memory
 
 // Visible pages of a token and the candidates [sink, sink + n) among them.
 struct Candidates {
@@ -60,105 +75,247 @@ __device__ __forceinline__ Candidates candidates(const SelectArgs& a, int pos) {
   return c;
 }
 
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&x)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
 __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectArgs a) {
-  __shared__ double qs[kScoreHeads][128];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // page_top waits by itself
+  // scores of one n8 group: [row][page], [row][page] of the magnitudes
+  __shared__ float tile[kScoreThreads / 32][2][16][9];
   const long long tg = blockIdx.x / a.chunks;
   const int chunk = static_cast<int>(blockIdx.x - tg * a.chunks);
-  const int t = static_cast<int>(tg / a.Hkv), g = static_cast<int>(tg - (long long)t * a.Hkv);
+  const int t0 = static_cast<int>(tg / a.Hkv);
+  const int g = static_cast<int>(tg - static_cast<long long>(t0) * a.Hkv);
   int s;
-  const Seq q = seq_of_token(a.q, t, s);
-  if (q.n == 0) return;
-  const Candidates cd = candidates(a, q.kv - q.n + (t - q.q0));
-  const int c0 = chunk * kScorePages;
-  if (cd.n <= a.top || c0 >= cd.n) return;          // nothing to rank
-  const int part = threadIdx.x & 3;
-  constexpr int kPer = kScorePages * 4 / kScoreThreads;
-  uint4 lo[kPer][4], hi[kPer][4];
+  const Seq q = seq_of_token(a.q, t0, s);
+  if (q.n == 0 || (t0 - q.q0) % a.tm != 0) return;        // another token's block has it
+  const int ntok = min(a.tm, q.q0 + q.n - t0);
+  const int pos0 = q.kv - q.n + (t0 - q.q0);
+  const Candidates cd = candidates(a, pos0 + ntok - 1);   // the last token sees most
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = chunk * kScorePages + warp * kWarpPages;
+  if (cd.n <= a.top || c0 >= cd.n) return;                // nothing to rank
+  const int part = lane & 3, r0 = lane >> 2;
+  const int mtiles = (a.group + 15) / 16;                 // 1 unless the group fills the rows
+  const int hrows = min(a.group, 16);
+  // lane l looks up page l of the warp's 32
+  const int cl = c0 + lane;
+  int mine = cl < cd.n ? phys_page(a.q, s, a.sink + cl) : 0;
+  if (mine < 0) mine = 0;
+  float best[kWarpPages / 8][4], mag[kWarpPages / 8][4];  // running maxima over m-tiles
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = c0 + i * (kScoreThreads / 4) + (threadIdx.x >> 2);
-    const int phys = c < cd.n ? phys_page(a.q, s, a.sink + c) : -1;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        a.summary + (static_cast<long long>(phys < 0 ? 0 : phys) * a.Hkv + g) * 256);
+  for (int i = 0; i < kWarpPages / 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      lo[i][j] = src[4 * j + part];
-      hi[i][j] = src[16 + 4 * j + part];
+    for (int e = 0; e < 4; ++e) best[i][e] = mag[i][e] = -INFINITY;
+  for (int mt = 0; mt < mtiles; ++mt) {
+    // the lane's two rows of q: (token, head) of rows r0 and r0 + 8
+    const uint4* src[2];
+    bool live[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = r0 + 8 * i;
+      const int ti = mtiles == 1 ? row / a.group : 0;
+      const int h = mtiles == 1 ? row - ti * a.group : 16 * mt + row;
+      live[i] = ti < ntok && h < a.group;
+      src[i] = reinterpret_cast<const uint4*>(
+          a.xq.at(0, live[i] ? t0 + ti : t0, g * a.group + (live[i] ? h : 0)));
     }
-  }
-  double best[kPer];
+    uint4 qa[2][4];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) best[i] = -INFINITY;
-  for (int h0 = 0; h0 < a.group; h0 += kScoreHeads) {
-    const int nh = min(kScoreHeads, a.group - h0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kScoreHeads * 128; i += kScoreThreads) {
-      const int h = i >> 7;
-      qs[h][i & 127] = h < nh ? static_cast<double>(__bfloat162float(
-                                    a.xq.at(0, t, g * a.group + h0 + h)[i & 127]))
-                              : 0.0;
-    }
-    __syncthreads();
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      double acc[kScoreHeads];
+      for (int j = 0; j < 4; ++j)
+        qa[i][j] = live[i] ? src[i][4 * j + part] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int h = 0; h < kScoreHeads; ++h) acc[h] = 0.0;
+    for (int n8 = 0; n8 < kWarpPages / 8; ++n8) {
+      const int phys = __shfl_sync(0xffffffffu, mine, 8 * n8 + r0);
+      const uint4* pg = reinterpret_cast<const uint4*>(
+          a.summary + (static_cast<long long>(phys) * a.Hkv + g) * 256);
+      uint4 lo[4], hi[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float l8[8], h8[8];
-        unpack8(lo[i][j], l8);
-        unpack8(hi[i][j], h8);
+        lo[j] = pg[4 * j + part];
+        hi[j] = pg[16 + 4 * j + part];
+      }
+      float u[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const double dl = l8[e], dh = h8[e];
-          const int d = 8 * (4 * j + part) + e;
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int h = 0; h < kScoreHeads; ++h) {
-            if (h < nh) {
-              const double x = qs[h][d];
-              acc[h] = fma(x, __double2hiint(x) >= 0 ? dh : dl, acc[h]);
-            }
+        for (int k = 0; k < 2; ++k) {
+          // k16 step: words 2k, 2k + 1 of this piece; rows r0 and r0 + 8
+          const uint32_t x[4] = {word(qa[0][j], 2 * k), word(qa[1][j], 2 * k),
+                                 word(qa[0][j], 2 * k + 1), word(qa[1][j], 2 * k + 1)};
+          uint32_t p[4], m[4], b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = max_bf16x2(x[e], 0u);
+            m[e] = min_bf16x2(x[e], 0u);
+            b[e] = x[e] & 0x7fff7fffu;
           }
+          const uint32_t l0 = word(lo[j], 2 * k), l1 = word(lo[j], 2 * k + 1);
+          const uint32_t h0 = word(hi[j], 2 * k), h1 = word(hi[j], 2 * k + 1);
+          mma_16816(u, p, h0, h1);
+          mma_16816(u, m, l0, l1);
+          mma_16816(v, b, max_bf16x2(l0 & 0x7fff7fffu, h0 & 0x7fff7fffu),
+                    max_bf16x2(l1 & 0x7fff7fffu, h1 & 0x7fff7fffu));
         }
       }
+      // a row without a head must not win
 #pragma unroll
-      for (int h = 0; h < kScoreHeads; ++h) {
-        if (h < nh) {
-          acc[h] += __shfl_xor_sync(0xffffffffu, acc[h], 1);
-          acc[h] += __shfl_xor_sync(0xffffffffu, acc[h], 2);
-          best[i] = fmax(best[i], acc[h]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        best[n8][e] = live[e >> 1] ? fmaxf(best[n8][e], u[e]) : best[n8][e];
+        mag[n8][e] = live[e >> 1] ? fmaxf(mag[n8][e], v[e]) : mag[n8][e];
       }
     }
   }
+  // maxima over the heads of a token: element e of the lane is row r0 + 8 (e / 2),
+  // page 2 part + e % 2 of its eight
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = c0 + i * (kScoreThreads / 4) + (threadIdx.x >> 2);
-    if (part == 0 && c < cd.n)
-      a.score[tg * a.q.per_seq + c] = static_cast<float>(best[i]) + 0.0f;   // -0 becomes +0
+  for (int n8 = 0; n8 < kWarpPages / 8; ++n8) {
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      tile[warp][0][r0 + 8 * (e >> 1)][2 * part + (e & 1)] = best[n8][e];
+      tile[warp][1][r0 + 8 * (e >> 1)][2 * part + (e & 1)] = mag[n8][e];
+    }
+    __syncwarp();
+    for (int i = lane; i < 8 * ntok; i += 32) {
+      const int ti = i >> 3, page = i & 7;
+      float x = -INFINITY, y = -INFINITY;
+      for (int h = 0; h < hrows; ++h) {
+        x = fmaxf(x, tile[warp][0][ti * hrows + h][page]);
+        y = fmaxf(y, tile[warp][1][ti * hrows + h][page]);
+      }
+      const int c = c0 + 8 * n8 + page;
+      if (c < cd.n)
+        a.score[(static_cast<long long>(t0 + ti) * a.Hkv + g) * a.q.per_seq + c] =
+            make_float2(x, y);
+    }
   }
 }
 
-// Order-preserving image of a float: larger value, larger integer.
+// Order-preserving image of a float: larger value, larger integer; -0 as 0.
 __device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t u = __float_as_uint(x);
+  const uint32_t u = __float_as_uint(x + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+
+struct TopSmem {
+  uint32_t keys[kTopKeys];
+  uint32_t hist[256];
+  uint32_t red[3][kTopThreads / 32];
+  uint32_t found[2];
+  unsigned long long sums[kTopThreads / 32];
+};
+
+// The key of rank `rank` (from 1, largest first) among key(i), i < n, where
+// use(i): eight bits at a time below the highest bit that the keys differ in.
+// Returns the key, and in `rank` its rank among the equal ones.  Every thread
+// of the block calls it.
+template <class Key, class Use>
+__device__ __forceinline__ uint32_t radix_rank(int n, Key key, Use use, uint32_t& rank,
+                                               TopSmem& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  for (int i = tid; i < n; i += kTopThreads)
+    if (use(i)) {
+      lo = min(lo, key(i));
+      hi = max(hi, key(i));
+    }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    sm.red[0][warp] = lo;
+    sm.red[1][warp] = hi;
+  }
+  __syncthreads();
+  lo = sm.red[0][lane & (kTopThreads / 32 - 1)];
+  hi = sm.red[1][lane & (kTopThreads / 32 - 1)];
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  uint32_t prefix = 0;                              // of key - lo
+  int bits = 32 - __clz(hi - lo);                   // bits not yet decided
+  while (bits > 0) {
+    const int shift = max(0, bits - 8);
+    const uint32_t mask = (1u << (bits - shift)) - 1u;
+    sm.hist[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kTopThreads) {
+      if (!use(i)) continue;
+      const uint32_t u = key(i) - lo;
+      if (bits == 32 || (u >> bits) == (prefix >> bits))
+        atomicAdd(&sm.hist[(u >> shift) & mask], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // lane l: digits 255 - 8 l down to 248 - 8 l
+      uint32_t c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        c[i] = sm.hist[255 - 8 * lane - i];
+        sum += c[i];
+      }
+      uint32_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      uint32_t above = incl - sum;
+      if (above < rank && rank <= incl) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (above < rank && rank <= above + c[i]) {
+            sm.found[0] = 255 - 8 * lane - i;
+            sm.found[1] = rank - above;
+          }
+          above += c[i];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= sm.found[0] << shift;
+    rank = sm.found[1];
+    bits = shift;
+  }
+  __syncthreads();                                  // found and red are written again
+  return prefix + lo;
 }
 
 __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t found[2];                     // digit, rank left within it
-  __shared__ unsigned long long sums[kTopThreads / 32];
+  __shared__ TopSmem sm;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long tg = blockIdx.x;
   const int t = static_cast<int>(tg / a.Hkv);
+  const int g = static_cast<int>(tg - static_cast<long long>(t) * a.Hkv);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int s;
   const Seq q = seq_of_token(a.q, t, s);
   if (q.n == 0) return;
   const Candidates cd = candidates(a, q.kv - q.n + (t - q.q0));
   int32_t* out = a.lists + tg * a.width;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int kept = min(cd.n, a.top);
   const int head = min(a.sink, cd.seen);            // sink pages
   const int tail = cd.seen - head - cd.n;           // recent pages
@@ -176,57 +333,112 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
       out[i] = i;
   }
   if (cd.n <= a.top || a.top == 0) return;
-  const float* score = a.score + tg * a.q.per_seq;
-  // the score of rank top: its digits from the highest down
-  uint32_t prefix = 0, rank = a.top;                // rank-th largest, from 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < cd.n; i += kTopThreads) {
-      const uint32_t u = ordered(score[i]);
-      if (shift == 24 || (u >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&hist[(u >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // lane l: digits 255 - 8 l .. 248 - 8 l
-      uint32_t n[8], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        n[i] = hist[255 - 8 * lane - i];
-        sum += n[i];
-      }
-      uint32_t incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      uint32_t above = incl - sum;
-      if (above < rank && rank <= incl) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (above < rank && rank <= above + n[i]) {
-            found[0] = 255 - 8 * lane - i;
-            found[1] = rank - above;
-          }
-          above += n[i];
-        }
-      }
-    }
-    __syncthreads();
-    prefix |= found[0] << shift;
-    rank = found[1];
-    __syncthreads();
+  float2* score = a.score + tg * a.q.per_seq;
+  float big = 0.f;
+  for (int i = tid; i < cd.n; i += kTopThreads) {
+    const float2 x = score[i];
+    big = fmaxf(big, x.y);
+    if (i < kTopKeys) sm.keys[i] = ordered(x.x);
   }
-  // every score above `prefix`, and the first `rank` equal to it
+  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+  if (lane == 0) sm.red[2][warp] = __float_as_uint(big);
+  __syncthreads();
+  big = __uint_as_float(
+      __reduce_max_sync(0xffffffffu, sm.red[2][lane & (kTopThreads / 32 - 1)]));
+  auto key = [&](int i) { return i < kTopKeys ? sm.keys[i] : ordered(score[i].x); };
+  uint32_t rank = a.top;
+  uint32_t edge = radix_rank(cd.n, key, [](int) { return true; }, rank, sm);
+  // keys above `top` are kept, below `bottom` are not
+  const float e2 = big * (1.0f / 8192.0f), mid = unordered(edge);
+  const uint32_t top = ordered(mid + e2), bottom = ordered(mid - e2);
+  uint32_t in = 0, between = 0;
+  for (int i = tid; i < cd.n; i += kTopThreads) {
+    const uint32_t u = key(i);
+    in += u > top;
+    between += u <= top && u >= bottom;
+  }
+  unsigned long long both = (static_cast<unsigned long long>(in) << 32) | between;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) both += __shfl_xor_sync(0xffffffffu, both, o);
+  if (lane == 0) sm.sums[warp] = both;
+  __syncthreads();
+  both = sm.sums[lane & (kTopThreads / 32 - 1)];
+#pragma unroll
+  for (int o = 1; o < kTopThreads / 32; o <<= 1) both += __shfl_xor_sync(0xffffffffu, both, o);
+  in = static_cast<uint32_t>(both >> 32);
+  between = static_cast<uint32_t>(both);
+  const uint32_t need = a.top - in;                 // of those between; at least one
+  // the smallest key kept, and how many of the pages that have it
+  uint32_t least = bottom, equal = 0xffffffffu;
+  if (between > need) {
+    // exact scores of the pages between, a warp each
+    __syncthreads();
+    for (int base = warp * 32; base < cd.n; base += kTopThreads) {
+      const uint32_t u = base + lane < cd.n ? key(base + lane) : 0u;
+      uint32_t todo = __ballot_sync(0xffffffffu, base + lane < cd.n && u <= top && u >= bottom);
+      while (todo) {
+        const int i = base + __ffs(todo) - 1;
+        todo &= todo - 1;
+        int phys = phys_page(a.q, s, a.sink + i);
+        if (phys < 0) phys = 0;
+        const __nv_bfloat16* pg = a.summary + (static_cast<long long>(phys) * a.Hkv + g) * 256;
+        float lo[4], hi[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          lo[d] = __bfloat162float(pg[4 * lane + d]);
+          hi[d] = __bfloat162float(pg[128 + 4 * lane + d]);
+        }
+        double best = -INFINITY;
+        for (int h = 0; h < a.group; ++h) {
+          const __nv_bfloat16* x = a.xq.at(0, t, g * a.group + h);
+          double sum = 0.0;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const float qd = __bfloat162float(x[4 * lane + d]);
+            sum += static_cast<double>(qd) * static_cast<double>(qd >= 0.f ? hi[d] : lo[d]);
+          }
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          best = fmax(best, sum);
+        }
+        // marked by a negative magnitude
+        if (lane == 0) score[i] = make_float2(static_cast<float>(best), -1.0f);
+      }
+    }
+    __syncthreads();
+    rank = need;
+    auto exact_key = [&](int i) { return ordered(score[i].x); };
+    auto marked = [&](int i) { return score[i].y < 0.f; };
+    least = radix_rank(cd.n, exact_key, marked, rank, sm);
+    equal = rank;
+  }
+  // pages above the border, and of those between the ones above `least` with
+  // the first `equal` that have it
+  const bool exact = between > need;
   const int per = (cd.n + kTopThreads - 1) / kTopThreads;
   const int i0 = min(cd.n, tid * per), i1 = min(cd.n, i0 + per);
-  unsigned long long mine = 0;                      // above in the high word, equal in the low
+  // 0 dropped, 1 kept, 2 equal to the least
+  auto verdict = [&](int i) -> int {
+    uint32_t u;
+    bool inside;
+    if (i < kTopKeys) {
+      u = sm.keys[i];
+      inside = u <= top && u >= bottom;
+    } else {
+      // a page summed exactly no longer has its fp32 sum, but its mark
+      const float2 x = score[i];
+      u = ordered(x.x);
+      inside = exact ? x.y < 0.f : u <= top && u >= bottom;
+    }
+    if (!inside) return u > top ? 1 : 0;
+    if (!exact) return 1;
+    if (i < kTopKeys) u = ordered(score[i].x);
+    return u > least ? 1 : u == least ? 2 : 0;
+  };
+  unsigned long long mine = 0;                      // kept in the high word, equal in the low
   for (int i = i0; i < i1; ++i) {
-    const uint32_t u = ordered(score[i]);
-    if (u > prefix) mine += 1ull << 32;
-    if (u == prefix) mine += 1ull;
+    const int vd = verdict(i);
+    mine += vd == 1 ? 1ull << 32 : static_cast<unsigned long long>(vd >> 1);
   }
   unsigned long long incl = mine;
 #pragma unroll
@@ -234,16 +446,19 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) sums[warp] = incl;
+  if (lane == 31) sm.sums[warp] = incl;
   __syncthreads();
   unsigned long long excl = incl - mine;
-  for (int w = 0; w < warp; ++w) excl += sums[w];
+  for (int w = 0; w < warp; ++w) excl += sm.sums[w];
   uint32_t gt = static_cast<uint32_t>(excl >> 32), eq = static_cast<uint32_t>(excl);
   for (int i = i0; i < i1; ++i) {
-    const uint32_t u = ordered(score[i]);
-    if (u > prefix || (u == prefix && eq < rank)) out[head + gt + min(eq, rank)] = a.sink + i;
-    gt += u > prefix;
-    eq += u == prefix;
+    const int vd = verdict(i);
+    const uint32_t at = gt + min(eq, equal);
+    if (vd == 1 || (vd == 2 && eq < equal)) {
+      if (at < static_cast<uint32_t>(a.top)) out[head + at] = a.sink + i;
+    }
+    gt += vd == 1;
+    eq += vd == 2;
   }
 }
 

@@ -139,8 +139,8 @@ PagedLayout paged_layout(const spa_paged_params* p) {
     return at;
   };
   lo.rec = take(kPagedGrid * sizeof(PagedRecord));
-  lo.part = take((size_t)2 * kPagedGrid * paged_slot_floats(256) * 4);
-  lo.score = take((size_t)p->tokens * p->heads_kv * p->pages_per_seq * 4);
+  lo.part = take((size_t)2 * kPagedGrid * kPagedSlotFloats * 4);
+  lo.score = take((size_t)p->tokens * p->heads_kv * p->pages_per_seq * 8);
   lo.total = off;
   return lo;
 }
@@ -174,13 +174,13 @@ bool launch_after(K kernel, dim3 grid, unsigned threads, cudaStream_t stream, co
   return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess;
 }
 
-template <int NT, bool LIST>
+template <bool LIST>
 bool launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                   const PagedAttnArgs& a, int combine_y, cudaStream_t stream) {
-  if (set_smem(paged_attn_kernel<NT, LIST>, kPagedSmemBytes) != cudaSuccess) return false;
-  paged_attn_kernel<NT, LIST><<<kPagedGrid, kPagedThreads, kPagedSmemBytes, stream>>>(tq, tk, tv, a);
+  if (set_smem(paged_attn_kernel<LIST>, kPagedSmemBytes) != cudaSuccess) return false;
+  paged_attn_kernel<LIST><<<kPagedGrid, kPagedThreads, kPagedSmemBytes, stream>>>(tq, tk, tv, a);
   if (cudaGetLastError() != cudaSuccess) return false;
-  return launch_after(paged_combine_kernel<NT>, dim3(kPagedGrid, combine_y), 128, stream, a);
+  return launch_after(paged_combine_kernel, dim3(kPagedGrid, combine_y), kCombineThreads, stream, a);
 }
 
 }  // namespace
@@ -304,7 +304,7 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
   a.q = seqs_of(p, cu_q, kv_lens, block_table, error_word);
   a.xq = rows_of(q);
   a.summary = static_cast<const __nv_bfloat16*>(summary);
-  a.score = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_layout(p).score);
+  a.score = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + paged_layout(p).score);
   a.lists = lists;
   a.counts = counts;
   a.Hkv = p->heads_kv;
@@ -313,6 +313,7 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
   a.local = p->local_pages;
   a.top = p->top_pages;
   a.width = a.sink + a.local + a.top;
+  a.tm = a.group <= 16 ? 16 / a.group : 1;
   const long long most = (long long)p->pages_per_seq - a.sink - a.local;   // candidates
   const long long tg = (long long)p->tokens * p->heads_kv;
   if (most > a.top && a.top > 0) {
@@ -368,26 +369,19 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
   a.part = reinterpret_cast<float*>(ws + lo.part);
   a.wait_ns = (uint64_t)(p->wait_limit_us ? p->wait_limit_us : 250000u) * 1000ull;
   a.debug = p->debug_flags;
-  // Two row tiles per key tile once the sequences bring more rows than one
-  // tile holds; with fewer, the second would be empty.
-  const long long rows = (long long)p->tokens * group / p->seqs;
-  const bool list = lists != nullptr;
-  const int nt = !list && rows > 128 ? 2 : 1;
   const uint64_t cache_rows =
       (uint64_t)a.pitch * (p->num_pages - 1) + (uint64_t)p->heads_kv * p->page_size;
   CUtensorMap tq, tk, tv;
-  if (!map_rows(&tq, q->data, p->heads_q, p->tokens, q->stride_head, q->stride_token, group,
-                nt == 2 ? a.tpt1 : 1) ||
+  if (!map_rows(&tq, q->data, p->heads_q, p->tokens, q->stride_head, q->stride_token, group) ||
       !map_2d(&tk, kBF16, 2, k_cache, 128, cache_rows, 64, p->page_size, kSW128) ||
       !map_2d(&tv, kBF16, 2, v_cache, 128, cache_rows, 64, p->page_size, kSW128))
     return SPA_ERR_CUDA;
-  // combine blocks beside one another: as many as the rows of a usual unit fill
-  long long cy = ((list ? group : rows) + 7) / 8;
-  if (cy < 1) cy = 1;
-  if (cy > 16 * nt) cy = 16 * nt;
-  const bool ok = list      ? launch_paged<1, true>(tq, tk, tv, a, (int)cy, stream)
-                  : nt == 1 ? launch_paged<1, false>(tq, tk, tv, a, (int)cy, stream)
-                            : launch_paged<2, false>(tq, tk, tv, a, (int)cy, stream);
+  // combine blocks beside one another: a warp per row of a usual unit
+  long long rows = lists ? group : (long long)p->tokens * group / p->seqs;
+  if (rows > kPagedSlotRows) rows = kPagedSlotRows;
+  const int cy = rows > 8 ? (int)(rows + 7) / 8 : 1;
+  const bool ok = lists ? launch_paged<true>(tq, tk, tv, a, cy, stream)
+                        : launch_paged<false>(tq, tk, tv, a, cy, stream);
   return ok ? SPA_OK : SPA_ERR_CUDA;
 }
 

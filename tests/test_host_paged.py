@@ -142,15 +142,15 @@ def test_empty_calls_launch_nothing():
 
 def test_tensor_checks_of_the_binding():
     x = torch.zeros(4, 4, 128, dtype=torch.bfloat16)
-    rows = binding._rows(x, (1, 4, 4, 128), "q")._obj
+    rows = binding._rows(x, 1, 4, 4, "q")._obj
     assert (rows.stride_batch, rows.stride_token, rows.stride_head) == (0, 512, 128)
     y = torch.zeros(2, 3, 5, 128, dtype=torch.bfloat16).transpose(1, 2)
-    rows = binding._rows(y, (2, 5, 3, 128), "q")._obj
+    rows = binding._rows(y, 2, 5, 3, "q")._obj
     assert (rows.stride_batch, rows.stride_token, rows.stride_head) == (1920, 128, 640)
     for bad, exc in ((x.half(), TypeError), (x[:3], ValueError),
                      (x.transpose(1, 2).contiguous().transpose(1, 2), ValueError)):
         with pytest.raises(exc):
-            binding._rows(bad, (1, 4, 4, 128), "q")
+            binding._rows(bad, 1, 4, 4, "q")
     p = paged()
     cache = torch.zeros(8, 2, 16, 128, dtype=torch.bfloat16)
     assert binding._cache(p, cache, "k") == cache.data_ptr()
@@ -162,11 +162,11 @@ def test_tensor_checks_of_the_binding():
     both = torch.zeros(8, 4, 16, 128, dtype=torch.bfloat16)
     assert binding._cache(paged(page_stride=4 * 16 * 128), both[:, 2:], "v") == both[:, 2:].data_ptr()
     with pytest.raises(ValueError):
-        binding._flat(torch.zeros(3, dtype=torch.int32), binding._I32, 4, "cu_q")
+        binding._i32(torch.zeros(3, dtype=torch.int32), 4, "cu_q")
     with pytest.raises(TypeError):
-        binding._flat(torch.zeros(4, dtype=torch.int64), binding._I32, 4, "cu_q")
+        binding._i32(torch.zeros(4, dtype=torch.int64), 4, "cu_q")
     with pytest.raises(ValueError):
-        binding._flat(torch.zeros(4, 2, dtype=torch.int32)[:, 0], binding._I32, 4, "cu_q")
+        binding._i32(torch.zeros(4, 2, dtype=torch.int32)[:, 0], 4, "cu_q")
     with pytest.raises(ValueError):                    # host memory
         spa.sparse_paged_status(torch.zeros(1, dtype=torch.int32), stream=0)
 
