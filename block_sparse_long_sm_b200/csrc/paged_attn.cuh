@@ -617,34 +617,32 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     const int row = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_col = 128u * hd, o_col = 256u + 128u * hd;
-    const int rt = row / a.group;                 // the row's token within a 128-row tile
-    const int rh = row - rt * a.group;            // its q head within the group
-    const bool row_fits = rt < a.tpt1;
     int sc = 0, oc[2] = {0, 0}, xc = 0;           // steps, accumulator uses, hand-overs
     bool ok = true;
-    PagedSeg sg;
-    for (int i = 0; ok && take(i, sg); ++i) {
-      const int tb = sg.tb, te = sg.te;
-      const bool duo = (sg.flags & kSegDuo) != 0;
-      const int ti = rt + (duo ? hd * a.tpt1 : 0);
-      const bool valid_row = row_fits && ti < sg.ntok;
-      const long long tok = static_cast<long long>(sg.tok0) + ti;
-      const int head = sg.g * a.group + rh;
-      if (sg.keys == 0) {
-        // no row of the unit sees a key
-        if (valid_row && (duo || hd == 0)) {
-          uint4* dst = reinterpret_cast<uint4*>(a.o.at(0, tok, head));
-          for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
-          if (a.lse) a.lse[tok * a.Hq + head] = -INFINITY;
-        }
-        continue;
+    for (int i = 0; ok; ++i) {
+      if (!warp_wait(bar_wfull(i % kPagedSegs), (i / kPagedSegs) & 1, wc)) break;
+      // The segment stays in the ring until its end and is read again there:
+      // its fields would not fit beside a row of scores in the registers.
+      const volatile PagedSeg& sg = segs[i % kPagedSegs];
+      const int te = sg.te, flags = sg.flags;
+      if (te < 0) break;
+      const bool duo = (flags & kSegDuo) != 0;
+      int t = sg.tb + (duo ? 0 : hd);
+      const bool two = !duo && te - t > (hd ^ 1);  // both accumulators belong to these rows
+      // keys of this thread's row, counted along the unit's key tiles
+      int seen;
+      bool busy;
+      {
+        const int rt = row / a.group;             // the row's token within a 128-row tile
+        const int ti = rt + (duo ? hd * a.tpt1 : 0);
+        const bool valid = rt < a.tpt1 && ti < sg.ntok;
+        seen = !valid ? 0 : LIST ? sg.keys : max(0, sg.pos0 + ti + 1);
+        busy = __any_sync(0xffffffffu, valid);
       }
-      // keys of the row, counted along the unit's key tiles
-      const int seen = !valid_row ? 0 : LIST ? sg.keys : max(0, sg.pos0 + ti + 1);
-      const bool busy = __any_sync(0xffffffffu, valid_row);
+      const bool none = sg.keys == 0;              // no row of the unit sees a key
       float m_used = -INFINITY, lsum = 0.f;
       bool started = false;
-      for (int t = duo ? tb : tb + hd; t < te; t += duo ? 1 : 2) {
+      for (; !none && t < te; t += duo ? 1 : 2) {
         if (!(ok = warp_wait(bar_sfull(hd), sc & 1, wc))) break;
         ++sc;
         tc_fence_after();
@@ -720,10 +718,26 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       }
       if (!ok) break;
       // ----------------------------------------------------- segment's end
-      const bool whole = (sg.flags & kSegWhole) != 0;
-      const bool two = !duo && te - tb > 1;       // both accumulators belong to these rows
-      const int use0 = oc[0]++, use1 = oc[1];
-      if (duo || two) ++oc[1];
+      const int use0 = oc[0], use1 = oc[1];
+      if (!none) {
+        ++oc[0];
+        if (duo || two) ++oc[1];
+      }
+      const bool whole = (flags & kSegWhole) != 0;
+      const int rt = row / a.group, ti = rt + (duo ? hd * a.tpt1 : 0);
+      const bool valid_row = rt < a.tpt1 && ti < sg.ntok;
+      const long long tok = static_cast<long long>(sg.tok0) + ti;
+      const int head = sg.g * a.group + (row - rt * a.group);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_wempty(i % kPagedSegs));
+      if (none) {
+        if (valid_row && (duo || hd == 0)) {
+          uint4* dst = reinterpret_cast<uint4*>(a.o.at(0, tok, head));
+          for (int k = 0; k < 16; ++k) dst[k] = make_uint4(0, 0, 0, 0);
+          if (a.lse) a.lse[tok * a.Hq + head] = -INFINITY;
+        }
+        continue;
+      }
       if (!duo && hd == 1) {
         if (!two) continue;
         // hand (m, l) to warpgroup 0, which joins the two accumulators; it has
@@ -739,7 +753,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (!(ok = warp_wait(bar_odone(hd), (hd ? use1 : use0) & 1, wc))) break;
       if (two && !(ok = warp_wait(bar_odone(1), use1 & 1, wc))) break;
       tc_fence_after();
-      float* part = a.part + (2LL * c + ((sg.flags & kSegStart) ? 1 : 0)) * kPagedSlotFloats;
+      float* part = a.part + (2LL * c + ((flags & kSegStart) ? 1 : 0)) * kPagedSlotFloats;
       const int prow = (duo ? hd * 128 : 0) + row;
       float fac0 = 1.f, fac1 = 0.f, m = m_used, l = lsum;
       if (two) {
