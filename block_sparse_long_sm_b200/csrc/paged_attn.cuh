@@ -11,16 +11,22 @@
 // + head.  Keys come in tiles of 128, a tile being 128 / page_size whole pages
 // found through the block table, one TMA box per page and 64 columns.
 //
-// Two ways through a segment, by the rows of its unit:
+// Three ways through a segment, by the rows of its unit:
 //   two row tiles   (more than 128 / group tokens)  A: the first 128 / group
 //           tokens, B: the next; both read every key tile, softmax warpgroup
 //           A / B works on its own rows;
 //   one row tile    the warpgroups take the key tiles in turn (even ones A, odd
 //           ones B), each with an accumulator of its own, and warpgroup A
-//           joins the two at the end.  A single token is bound by the bytes of
-//           K and V, and two independent chains of tiles hide the latency of
-//           one another's softmax.
-// Either way step j of a segment (a run of key tiles) uses score slot,
+//           joins the two at the end: two independent chains of tiles hide the
+//           latency of one another's softmax;
+//   few rows        (at most 16: one token, or a few of a small group)  a
+//           128-row product would be empty for the most part, and its softmax
+//           keeps one warp of four busy; instead each of the eight warps takes
+//           16 keys of every tile with mma.sync m16n8k16, from the same shared
+//           memory, (max, sum, O) in its registers, and the eight are joined
+//           at the end.  Bound by the bytes of K and V: 64 KB a tile against
+//           256 such products.
+// In the first two step j of a segment (a run of key tiles) uses score slot,
 // accumulator and warpgroup j & 1, in the order
 //   S_0, S_1, PV_0, S_2, PV_1, S_3, PV_2, ...
 // so the tensor core has one product to do while the other slot's softmax runs.
@@ -88,10 +94,20 @@ constexpr int kPagedSegs = 4;
 constexpr int kSegDuo = 1;      // two row tiles
 constexpr int kSegStart = 2;    // holds the unit's first tile
 constexpr int kSegWhole = 4;    // holds all of them
+constexpr int kSegFew = 8;      // at most kFewRows rows
+// Q buffers (each 32 KB): both for two row tiles, one of them in turn for one,
+// both as the exchange area of few rows
+constexpr int kSegBuf = 16;     // the one in turn
+constexpr int kSegPar = 32;     // << i: parity of buffer i's use
+constexpr int kSegOld = 128;    // << i: it was used before
+constexpr int kFewRows = 16;
+// Arrivals that free a K, V or Q buffer: of the eight softmax warps and the MMA
+// warp when rows are few, else of the MMA's commit, which counts for all.
+constexpr uint32_t kReaders = 9;
 
 struct PagedAttnArgs {
   Seqs q;
-  Rows o;
+  Rows xq, o;
   float* lse;                // [T][Hq] or null
   const int32_t* lists;      // [T][Hkv][width] or null
   const int32_t* counts;     // [T][Hkv]
@@ -271,11 +287,250 @@ struct PagedWalk {
   }
 };
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+// Float index of (row, column) of a warp's 16 x 128 exchange area: groups of
+// eight columns are permuted by the row, so that neither the fragments' 8-byte
+// stores nor the rows' 16-byte loads meet in a bank.
+__device__ __forceinline__ int few_at(int row, int col) {
+  return row * 128 + (col ^ ((row & 7) << 3));
+}
+
+// Barriers, 8 bytes each from b0.
+struct PagedBars {
+  uint32_t b0;
+  __device__ __forceinline__ uint32_t at(int i) const { return b0 + 8u * i; }
+  __device__ __forceinline__ uint32_t kfull(int s) const { return at(s); }
+  __device__ __forceinline__ uint32_t kempty(int s) const { return at(3 + s); }
+  __device__ __forceinline__ uint32_t vfull(int s) const { return at(6 + s); }
+  __device__ __forceinline__ uint32_t vempty(int s) const { return at(8 + s); }
+  __device__ __forceinline__ uint32_t vclean(int s) const { return at(10 + s); }
+  __device__ __forceinline__ uint32_t sfull(int h) const { return at(12 + h); }
+  __device__ __forceinline__ uint32_t pfull(int h) const { return at(14 + h); }
+  __device__ __forceinline__ uint32_t odone(int h) const { return at(16 + h); }
+  __device__ __forceinline__ uint32_t ofree(int h) const { return at(18 + h); }
+  __device__ __forceinline__ uint32_t qfull(int i) const { return at(20 + i); }
+  __device__ __forceinline__ uint32_t qfree(int i) const { return at(22 + i); }
+  __device__ __forceinline__ uint32_t wfull(int i) const { return at(24 + i); }
+  __device__ __forceinline__ uint32_t wempty(int i) const { return at(28 + i); }
+  __device__ __forceinline__ uint32_t xch() const { return at(32); }
+  __device__ __forceinline__ uint32_t drain() const { return at(33); }
+  __device__ __forceinline__ uint32_t stall() const { return at(34); }
+  __device__ __forceinline__ uint32_t few() const { return at(35); }
+};
+static_assert(kPagedKStages == 3 && kPagedVStages == 2, "barrier numbers");
+// Offsets behind the barriers (36 of them).
+constexpr int kPagedTmem = 304, kPagedSegRing = 320, kPagedFind = 512, kPagedMl = 1024;
+
+// A segment of few rows (see above), by one of the eight warps; kt: the CTA's
+// tiles before it, parity: of this segment's exchange, uses1: of accumulator 1
+// before it.  False when a wait gave up.  A function of its own, so that its
+// registers and those of the 128-row softmax are allotted apart.
+template <bool LIST>
+__device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const PagedSeg sg, uint8_t* smem,
+                                         uint32_t s_base, uint32_t b0, const WaitCtx wc, int kt,
+                                         uint32_t parity, int uses1) {
+  const PagedBars bars{b0};
+  volatile float* ml = reinterpret_cast<volatile float*>(
+      smem + (2 + kPagedKStages + kPagedVStages) * kTileBytes + kPagedMl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
+  const int tb = sg.tb, te = sg.te, keys = sg.keys, g = sg.g, tok0 = sg.tok0, flags = sg.flags;
+  const int nrows = sg.ntok * a.group;
+  const int r0 = lane >> 2, c2 = 2 * (lane & 3);
+  int seen[2];
+  uint32_t qf[8][4];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    // rows r0 and r0 + 8; rows behind the last are zero
+    const int rr = r0 + 8 * e, ti = rr / a.group;
+    const bool on = rr < nrows;
+    seen[e] = !on ? 0 : LIST ? keys : max(0, sg.pos0 + ti + 1);
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        a.xq.at(0, tok0 + (on ? ti : 0), g * a.group + (on ? rr - ti * a.group : 0)));
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      qf[ks][e] = on ? src[(16 * ks + c2) >> 1] : 0u;
+      qf[ks][2 + e] = on ? src[(16 * ks + 8 + c2) >> 1] : 0u;
+    }
+  }
+  float acc[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+  for (int t = tb; t < te; ++t, ++kt) {
+    const int ks_ = kt % kPagedKStages, vs_ = kt % kPagedVStages;
+    const int left = keys - 128 * t - 16 * warp;   // keys from this warp's sixteen on
+    if (!warp_wait(bars.kfull(ks_), (kt / kPagedKStages) & 1, wc)) return false;
+    uint32_t pf[4];
+    if (left > 0) {
+      float sc2[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc2[n][e] = 0.f;
+      // matrix i of a load: key half i / 2 (8 keys each), 16-byte chunk i % 2
+      const int key = 16 * warp + ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        uint32_t kf[4];
+        const int chunk = (2 * ks + ((lane >> 3) & 1)) & 7;
+        ldsm4(kf, (s_base + (2u + ks_) * kTileBytes) + (ks >> 2) * kHalfBytes + key * 128u +
+                      ((chunk ^ (key & 7)) << 4));
+        mma_16816(sc2[0], qf[ks], kf[0], kf[1]);
+        mma_16816(sc2[1], qf[ks], kf[2], kf[3]);
+      }
+      const int k0 = 128 * t + 16 * warp + c2;
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (k0 + 8 * n + (e & 1) >= seen[e >> 1]) sc2[n][e] = -INFINITY;
+          mx[e >> 1] = fmaxf(mx[e >> 1], sc2[n][e]);
+        }
+      float fac[2];
+      bool grow = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2)) * a.sl2;
+        fac[e] = 1.f;
+        if (mx[e] > m[e] + 8.0f) {              // as above: the maximum may lag
+          fac[e] = fast_exp2(m[e] - mx[e]);
+          m[e] = mx[e];
+          l[e] *= fac[e];
+          grow = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] *= fac[e >> 1];
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float nm = m[e] == -INFINITY ? 0.f : -m[e];
+          const float p0 = fast_exp2(fmaf(sc2[n][2 * e], a.sl2, nm));
+          const float p1 = fast_exp2(fmaf(sc2[n][2 * e + 1], a.sl2, nm));
+          l[e] += p0 + p1;
+          pf[2 * n + e] = pack_bf16x2(p0, p1);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.kempty(ks_));
+    if (!warp_wait(bars.vfull(vs_), (kt / kPagedVStages) & 1, wc)) return false;
+    if (!warp_wait(bars.vclean(vs_), (kt / kPagedVStages) & 1, wc)) return false;
+    if (left > 0) {
+      // matrix i: key half i % 2, 16-byte chunk i / 2 of a pair
+      const int key = 16 * warp + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t vf[4];
+        const int chunk = (2 * j + (lane >> 4)) & 7;
+        ldsm4_t(vf, (s_base + (2u + kPagedKStages + vs_) * kTileBytes) + (j >> 2) * kHalfBytes + key * 128u +
+                        ((chunk ^ (key & 7)) << 4));
+        mma_16816(acc[2 * j], pf, vf[0], vf[1]);
+        mma_16816(acc[2 * j + 1], pf, vf[2], vf[3]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.vempty(vs_));
+  }
+  // join the eight warps: the Q buffers are the exchange area
+  for (int b = 0; b < 2; ++b)
+    if (!warp_wait(bars.qfull(b), (flags & (kSegPar << b)) ? 1 : 0, wc)) return false;
+  // (warpgroup 0 may still read ml for an earlier segment's second accumulator)
+  if (warp >= 4 && uses1 > 0 && !warp_wait(bars.ofree(1), (uses1 - 1) & 1, wc)) return false;
+  float* area = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    const int rr = r0 + 8 * e;
+    if (rr < nrows) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        *reinterpret_cast<float2*>(area + warp * 2048 + few_at(rr, 8 * j + c2)) =
+            make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
+      if ((lane & 3) == 0) {
+        ml[warp * 16 + rr] = m[e];
+        ml[128 + warp * 16 + rr] = l[e];
+      }
+    }
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bars.few());
+  if (!warp_wait(bars.few(), parity, wc)) return false;
+  float* part = a.part + (2LL * c + ((flags & kSegStart) ? 1 : 0)) * kPagedSlotFloats;
+  const bool whole = (flags & kSegWhole) != 0;
+  for (int rr = warp; rr < nrows; rr += 8) {
+    float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) mm = fmaxf(mm, ml[w * 16 + rr]);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const float mw = ml[w * 16 + rr];
+      const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - mm);
+      ll = fmaf(ml[128 + w * 16 + rr], f, ll);
+      const float4 x = *reinterpret_cast<const float4*>(area + w * 2048 + few_at(rr, 4 * lane));
+      y.x = fmaf(x.x, f, y.x);
+      y.y = fmaf(x.y, f, y.y);
+      y.z = fmaf(x.z, f, y.z);
+      y.w = fmaf(x.w, f, y.w);
+    }
+    const int ti = rr / a.group;
+    const long long tok = static_cast<long long>(tok0) + ti;
+    const int head = g * a.group + (rr - ti * a.group);
+    if (whole) {
+      const float inv = ll > 0.f ? 1.0f / ll : 0.f;
+      uint2 z;
+      z.x = pack_bf16x2(y.x * inv, y.y * inv);
+      z.y = pack_bf16x2(y.z * inv, y.w * inv);
+      *reinterpret_cast<uint2*>(a.o.at(0, tok, head) + 4 * lane) = z;
+      if (a.lse && lane == 0)
+        a.lse[tok * a.Hq + head] =
+            ll > 0.f ? mm * 0.69314718055994531f + logf(ll) : -INFINITY;
+    } else {
+      *reinterpret_cast<float4*>(part + rr * 128 + 4 * lane) = y;
+      if (lane == 0) {
+        part[128 * kPagedSlotRows + rr] = mm;
+        part[129 * kPagedSlotRows + rr] = ll;
+      }
+    }
+  }
+  __syncwarp();
+  if (lane == 0) {
+    mbar_arrive(bars.qfree(0));
+    mbar_arrive(bars.qfree(1));
+  }
+  return true;
+}
+
 template <bool LIST>
 __global__ void __launch_bounds__(kPagedThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const PagedAttnArgs a) {
+                  const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ PagedAttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -285,54 +540,42 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
   auto s_v = [&](int st) { return s_base + (2u + kPagedKStages + st) * kTileBytes; };
   uint8_t* ctl = smem + (2 + kPagedKStages + kPagedVStages) * kTileBytes;
   const uint32_t b0 = smem_u32(ctl);
-  auto bar_kfull = [&](int s) { return b0 + 8u * s; };
-  auto bar_kempty = [&](int s) { return b0 + 8u * (3 + s); };
-  auto bar_vfull = [&](int s) { return b0 + 8u * (6 + s); };
-  auto bar_vempty = [&](int s) { return b0 + 8u * (8 + s); };
-  auto bar_vclean = [&](int s) { return b0 + 8u * (10 + s); };
-  auto bar_sfull = [&](int h) { return b0 + 8u * (12 + h); };
-  auto bar_pfull = [&](int h) { return b0 + 8u * (14 + h); };
-  auto bar_odone = [&](int h) { return b0 + 8u * (16 + h); };
-  auto bar_ofree = [&](int h) { return b0 + 8u * (18 + h); };
-  auto bar_qfull = [&](int i) { return b0 + 8u * (20 + i); };
-  auto bar_qfree = [&](int i) { return b0 + 8u * (22 + i); };
-  auto bar_wfull = [&](int i) { return b0 + 8u * (24 + i); };
-  auto bar_wempty = [&](int i) { return b0 + 8u * (28 + i); };
-  const uint32_t bar_xch = b0 + 8u * 32, bar_drain = b0 + 8u * 33, bar_stall = b0 + 8u * 34;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(ctl + 288);
-  PagedSeg* segs = reinterpret_cast<PagedSeg*>(ctl + 320);
+  const PagedBars bars{b0};
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(ctl + kPagedTmem);
   volatile uint32_t* abort_flag = tmem_holder + 1;
-  FindSmem& find = *reinterpret_cast<FindSmem*>(ctl + 512);
-  static_assert(sizeof(FindSmem) <= 512, "search area");
-  volatile float* ml = reinterpret_cast<volatile float*>(ctl + 1024);   // slot 1's m, l [128]
+  PagedSeg* segs = reinterpret_cast<PagedSeg*>(ctl + kPagedSegRing);
+  FindSmem& find = *reinterpret_cast<FindSmem*>(ctl + kPagedFind);
+  static_assert(sizeof(FindSmem) <= kPagedMl - kPagedFind, "search area");
+  volatile float* ml = reinterpret_cast<volatile float*>(ctl + kPagedMl);   // slot 1's m, l [128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine waits by itself
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPagedKStages; ++i) {
-      mbar_init(bar_kfull(i), 1);
-      mbar_init(bar_kempty(i), 1);
+      mbar_init(bars.kfull(i), 1);
+      mbar_init(bars.kempty(i), kReaders);
     }
     for (int i = 0; i < kPagedVStages; ++i) {
-      mbar_init(bar_vfull(i), 1);
-      mbar_init(bar_vempty(i), 1);
-      mbar_init(bar_vclean(i), 1);
+      mbar_init(bars.vfull(i), 1);
+      mbar_init(bars.vempty(i), kReaders);
+      mbar_init(bars.vclean(i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_sfull(i), 1);
-      mbar_init(bar_pfull(i), 128);
-      mbar_init(bar_odone(i), 1);
-      mbar_init(bar_ofree(i), 128);
-      mbar_init(bar_qfull(i), 1);
-      mbar_init(bar_qfree(i), 1);
+      mbar_init(bars.sfull(i), 1);
+      mbar_init(bars.pfull(i), 128);
+      mbar_init(bars.odone(i), 1);
+      mbar_init(bars.ofree(i), i == 0 ? 256 : 128);
+      mbar_init(bars.qfull(i), 1);
+      mbar_init(bars.qfree(i), kReaders);
     }
     for (int i = 0; i < kPagedSegs; ++i) {
-      mbar_init(bar_wfull(i), 1);
-      mbar_init(bar_wempty(i), 11);     // loads, MMA, clearing, eight softmax warps
+      mbar_init(bars.wfull(i), 1);
+      mbar_init(bars.wempty(i), 11);     // loads, MMA, clearing, eight softmax warps
     }
-    mbar_init(bar_xch, 128);
-    mbar_init(bar_drain, 1);
-    mbar_init(bar_stall, 1);
+    mbar_init(bars.few(), 8);
+    mbar_init(bars.xch(), 128);
+    mbar_init(bars.drain(), 1);
+    mbar_init(bars.stall(), 1);
     *abort_flag = 0u;
     fence_barrier_init();
     prefetch_tensormap(&tm_q);
@@ -380,10 +623,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
   // Segment i of the piece, copied out of the ring; false at its end.
   auto take = [&](int i, PagedSeg& sg) -> bool {
     const int r = i % kPagedSegs;
-    if (!warp_wait(bar_wfull(r), (i / kPagedSegs) & 1, wc)) return false;
+    if (!warp_wait(bars.wfull(r), (i / kPagedSegs) & 1, wc)) return false;
     sg = segs[r];
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar_wempty(r));
+    if (lane == 0) mbar_arrive(bars.wempty(r));
     return sg.te >= 0;
   };
 
@@ -393,28 +636,32 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       // ----------------------------------------------------------- loads
       const int ppt = 128 >> a.q.shift;             // pages per tile
       const uint32_t page_half = 128u * a.q.page;   // bytes of a page's 64 columns
-      int kt = 0, qu[2] = {0, 0}, qn = 0;           // key tiles, Q buffer uses, next buffer
+      int kt = 0, qlast[2] = {-1, -1};              // key tiles; parity of the Q loads in flight
       bool ok = true;
       PagedSeg sg;
       for (int i = 0; ok && take(i, sg); ++i) {
         if (sg.keys == 0) continue;
-        // Q: both buffers for two row tiles, else the buffers in turn
-        const bool duo = (sg.flags & kSegDuo) != 0;
-        const int first = duo ? 0 : qn, tiles = duo ? 2 : 1;
-        if (!duo) qn ^= 1;
-        for (int q = 0; ok && q < tiles; ++q) {
-          const int buf = first + q;
-          if (qu[buf] > 0 && !(ok = warp_wait(bar_qfree(buf), (qu[buf] - 1) & 1, wc))) break;
+        const bool duo = (sg.flags & kSegDuo) != 0, few = (sg.flags & kSegFew) != 0;
+        for (int buf = 0; buf < 2; ++buf) {
+          if (!duo && !few && buf != ((sg.flags & kSegBuf) ? 1 : 0)) continue;
+          const int par = (sg.flags & (kSegPar << buf)) ? 1 : 0;
+          if ((sg.flags & (kSegOld << buf)) && !(ok = warp_wait(bars.qfree(buf), par ^ 1, wc))) break;
+          if (few) {                                // nothing to load: the area is free
+            if (lane == 0) mbar_arrive(bars.qfull(buf));
+            qlast[buf] = -1;
+            continue;
+          }
+          const int q = duo ? buf : 0;
           const int tok = sg.tok0 + q * a.tpt1;
           const int n = min(a.tpt1, sg.ntok - q * a.tpt1);
-          if (lane == 0) mbar_arrive_expect_tx(bar_qfull(buf), n * a.group * 256u);
+          if (lane == 0) mbar_arrive_expect_tx(bars.qfull(buf), n * a.group * 256u);
           __syncwarp();
           for (int k = lane; k < n; k += 32) {
             const uint32_t at = s_q(buf) + k * a.group * 128u;
-            tma_load_3d(at, &tm_q, bar_qfull(buf), 0, sg.g * a.group, tok + k);
-            tma_load_3d(at + kHalfBytes, &tm_q, bar_qfull(buf), 64, sg.g * a.group, tok + k);
+            tma_load_3d(at, &tm_q, bars.qfull(buf), 0, sg.g * a.group, tok + k);
+            tma_load_3d(at + kHalfBytes, &tm_q, bars.qfull(buf), 64, sg.g * a.group, tok + k);
           }
-          ++qu[buf];
+          qlast[buf] = par;
         }
         if (!ok) break;
         __syncwarp();
@@ -446,26 +693,26 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           const int row = phys * a.pitch + (sg.g << a.q.shift);
           const int ks = kt % kPagedKStages, vs = kt % kPagedVStages;
           const int ku = kt / kPagedKStages, vu = kt / kPagedVStages;
-          if (ku > 0 && !(ok = warp_wait(bar_kempty(ks), (ku - 1) & 1, wc))) break;
-          if (lane == 0) mbar_arrive_expect_tx(bar_kfull(ks), live * 2u * page_half);
+          if (ku > 0 && !(ok = warp_wait(bars.kempty(ks), (ku - 1) & 1, wc))) break;
+          if (lane == 0) mbar_arrive_expect_tx(bars.kfull(ks), live * 2u * page_half);
           __syncwarp();
           if (phys >= 0) {
             const uint32_t at = s_k(ks) + lane * page_half;
-            tma_load_2d(at, &tm_k, bar_kfull(ks), 0, row);
-            tma_load_2d(at + kHalfBytes, &tm_k, bar_kfull(ks), 64, row);
+            tma_load_2d(at, &tm_k, bars.kfull(ks), 0, row);
+            tma_load_2d(at + kHalfBytes, &tm_k, bars.kfull(ks), 64, row);
           }
           __syncwarp();
-          if (vu > 0 && !(ok = warp_wait(bar_vempty(vs), (vu - 1) & 1, wc))) {
+          if (vu > 0 && !(ok = warp_wait(bars.vempty(vs), (vu - 1) & 1, wc))) {
             // K of this tile is in flight and counted: drain it below
             ++kt;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(bar_vfull(vs), live * 2u * page_half);
+          if (lane == 0) mbar_arrive_expect_tx(bars.vfull(vs), live * 2u * page_half);
           __syncwarp();
           if (phys >= 0) {
             const uint32_t at = s_v(vs) + lane * page_half;
-            tma_load_2d(at, &tm_v, bar_vfull(vs), 0, row);
-            tma_load_2d(at + kHalfBytes, &tm_v, bar_vfull(vs), 64, row);
+            tma_load_2d(at, &tm_v, bars.vfull(vs), 0, row);
+            tma_load_2d(at + kHalfBytes, &tm_v, bars.vfull(vs), 64, row);
           }
           __syncwarp();
         }
@@ -474,33 +721,52 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       // (immediate in normal operation, bounded after an abort)
       if (lane == 0) {
         for (int i = max(0, kt - kPagedKStages); i < kt; ++i)
-          mbar_drain(bar_kfull(i % kPagedKStages), (i / kPagedKStages) & 1, a.wait_ns);
+          mbar_drain(bars.kfull(i % kPagedKStages), (i / kPagedKStages) & 1, a.wait_ns);
         for (int i = max(0, kt - kPagedVStages); i < kt; ++i)
-          mbar_drain(bar_vfull(i % kPagedVStages), (i / kPagedVStages) & 1, a.wait_ns);
+          mbar_drain(bars.vfull(i % kPagedVStages), (i / kPagedVStages) & 1, a.wait_ns);
         for (int i = 0; i < 2; ++i)
-          if (qu[i] > 0) mbar_drain(bar_qfull(i), (qu[i] - 1) & 1, a.wait_ns);
+          if (qlast[i] >= 0) mbar_drain(bars.qfull(i), qlast[i], a.wait_ns);
       }
     } else if (warp == 9) {
       // ------------------------------------------------------- MMA issuer
       bool ok = true;
-      if (a.debug & 1u) ok = warp_wait(bar_stall, 0, wc);   // never signalled: test hook
-      int kt = 0, qn = 0, qu[2] = {0, 0}, pc[2] = {0, 0}, oc[2] = {0, 0};
+      if (a.debug & 1u) ok = warp_wait(bars.stall(), 0, wc);   // never signalled: test hook
+      int kt = 0, pc[2] = {0, 0}, oc[2] = {0, 0};
+      auto commit_all = [](uint32_t bar) {
+        mbar_arrive_n(bar, kReaders - 1);
+        mma_commit(bar);
+      };
       PagedSeg sg;
       for (int i = 0; ok && take(i, sg); ++i) {
         if (sg.keys == 0) continue;
+        if (sg.flags & kSegFew) {
+          // No product of this warp, but it sees every phase of the barriers it
+          // will wait on again, and holds up the next one until it has: a wait
+          // tells phase n only from n - 1.
+          for (int b = 0; ok && b < 2; ++b) {
+            ok = warp_wait(bars.qfull(b), (sg.flags & (kSegPar << b)) ? 1 : 0, wc);
+            if (ok && lane == 0) mbar_arrive(bars.qfree(b));
+          }
+          for (int t = sg.tb; ok && t < sg.te; ++t, ++kt) {
+            const int ks = kt % kPagedKStages, vs = kt % kPagedVStages;
+            if (!(ok = warp_wait(bars.kfull(ks), (kt / kPagedKStages) & 1, wc))) break;
+            if (lane == 0) mbar_arrive(bars.kempty(ks));
+            if (!(ok = warp_wait(bars.vfull(vs), (kt / kPagedVStages) & 1, wc))) break;
+            if (lane == 0) mbar_arrive(bars.vempty(vs));
+          }
+          continue;
+        }
         if (lane == 0) {
           const int duo = (sg.flags & kSegDuo) ? 1 : 0;
           const int tiles = sg.te - sg.tb, steps = tiles << duo;
-          const int buf = qn;
-          if (!duo) qn ^= 1;
+          const int buf = (sg.flags & kSegBuf) ? 1 : 0;
           auto qk = [&](int j) -> bool {
             const int h = j & 1, k = kt + (j >> duo), st = k % kPagedKStages;
             const int qb = duo ? h : buf;
             if (j < 2 && (duo || j == 0)) {
-              if (!mbar_wait(bar_qfull(qb), qu[qb] & 1, wc)) return false;
-              ++qu[qb];
+              if (!mbar_wait(bars.qfull(qb), (sg.flags & (kSegPar << qb)) ? 1 : 0, wc)) return false;
             }
-            if (!mbar_wait(bar_kfull(st), (k / kPagedKStages) & 1, wc)) return false;
+            if (!mbar_wait(bars.kfull(st), (k / kPagedKStages) & 1, wc)) return false;
             tc_fence_after();
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
@@ -508,21 +774,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
               mma_bf16_ss(tmem + 128u * h, smem_desc_sw128(s_q(qb) + off, 16),
                           smem_desc_sw128(s_k(st) + off, 16), kIdescQK, ks > 0 ? 1u : 0u);
             }
-            mma_commit(bar_sfull(h));
-            if (!duo || h == 1) mma_commit(bar_kempty(st));
-            if (j + 1 + duo >= steps) mma_commit(bar_qfree(qb));
+            mma_commit(bars.sfull(h));
+            if (!duo || h == 1) commit_all(bars.kempty(st));
+            if (j + 1 + duo >= steps) commit_all(bars.qfree(qb));
             return true;
           };
           auto pv = [&](int j) -> bool {
             const int h = j & 1, k = kt + (j >> duo), st = k % kPagedVStages;
             const bool first = j < 2;
-            if (!mbar_wait(bar_pfull(h), pc[h] & 1, wc)) return false;
+            if (!mbar_wait(bars.pfull(h), pc[h] & 1, wc)) return false;
             ++pc[h];
-            if (!mbar_wait(bar_vfull(st), (k / kPagedVStages) & 1, wc)) return false;
-            if (!mbar_wait(bar_vclean(st), (k / kPagedVStages) & 1, wc)) return false;
+            if (!mbar_wait(bars.vfull(st), (k / kPagedVStages) & 1, wc)) return false;
+            if (!mbar_wait(bars.vclean(st), (k / kPagedVStages) & 1, wc)) return false;
             if (first) {
               // this accumulator of the segment before has been read
-              if (oc[h] > 0 && !mbar_wait(bar_ofree(h), (oc[h] - 1) & 1, wc)) return false;
+              if (oc[h] > 0 && !mbar_wait(bars.ofree(h), (oc[h] - 1) & 1, wc)) return false;
               ++oc[h];
             }
             tc_fence_after();
@@ -532,8 +798,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                           smem_desc_sw128(s_v(st) + ks * 2048u, kHalfBytes), kIdescPV,
                           (!first || ks > 0) ? 1u : 0u);
             }
-            if (!duo || h == 1) mma_commit(bar_vempty(st));
-            if (j + 2 >= steps) mma_commit(bar_odone(h));
+            if (!duo || h == 1) commit_all(bars.vempty(st));
+            if (j + 2 >= steps) mma_commit(bars.odone(h));
             return true;
           };
           for (int j = 0; ok && j < 2 && j < steps; ++j) ok = qk(j);
@@ -541,14 +807,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
             ok = pv(j);
             if (ok && j + 2 < steps) ok = qk(j + 2);
           }
-          kt += tiles;
         }
+        kt += sg.te - sg.tb;
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
       // every MMA issued by this thread has completed once this arrives
       if (lane == 0) {
-        mma_commit(bar_drain);
-        mbar_drain(bar_drain, 0, a.wait_ns);
+        mma_commit(bars.drain());
+        mbar_drain(bars.drain(), 0, a.wait_ns);
       }
       __syncwarp();
     } else if (warp == 10) {
@@ -560,7 +826,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         if (sg.keys == 0) continue;
         for (int t = sg.tb; t < sg.te; ++t, ++kt) {
           const int st = kt % kPagedVStages;
-          if (!(ok = warp_wait(bar_vfull(st), (kt / kPagedVStages) & 1, wc))) break;
+          if (!(ok = warp_wait(bars.vfull(st), (kt / kPagedVStages) & 1, wc))) break;
           const int valid = sg.keys - 128 * t;
           if (valid < 128) {
             // whole 128-byte rows, so the swizzle within a row does not matter
@@ -572,7 +838,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
             fence_proxy_async_smem();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_vclean(st));
+          if (lane == 0) mbar_arrive(bars.vclean(st));
         }
       }
     } else if (lane == 0) {
@@ -581,14 +847,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       walk.x0 = f.total * c / G;
       walk.x1 = f.total * (c + 1) / G;
       PagedRecord mine{-1, 0, 0, 0};
+      int qn = 0, qu[2] = {0, 0};                   // next Q buffer, uses of each
       int i = 0;
       bool ok = true;
       auto hand = [&](const PagedSeg& sg) {
         const int r = i % kPagedSegs;
-        if (i >= kPagedSegs && !(ok = mbar_wait(bar_wempty(r), (i / kPagedSegs - 1) & 1, wc)))
+        if (i >= kPagedSegs && !(ok = mbar_wait(bars.wempty(r), (i / kPagedSegs - 1) & 1, wc)))
           return;
         segs[r] = sg;
-        mbar_arrive(bar_wfull(r));
+        mbar_arrive(bars.wfull(r));
         ++i;
       };
       if (c < G && walk.x0 < walk.x1 && f.s >= 0) {
@@ -601,8 +868,19 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
             mine.tok0 = walk.tok0;
             mine.ntok = walk.ntok;
           }
-          const int flags = (walk.w == 2 ? kSegDuo : 0) | (tb == 0 ? kSegStart : 0) |
-                            (tb == 0 && te == walk.nt ? kSegWhole : 0);
+          int flags = (tb == 0 ? kSegStart : 0) | (tb == 0 && te == walk.nt ? kSegWhole : 0);
+          if (walk.w == 2) flags |= kSegDuo;
+          if (walk.ntok * a.group <= kFewRows) flags |= kSegFew;
+          if (walk.keys > 0) {
+            const bool both = (flags & (kSegDuo | kSegFew)) != 0;
+            if (!both) flags |= qn ? kSegBuf : 0;
+            for (int b = 0; b < 2; ++b) {
+              if (!both && b != qn) continue;
+              flags |= ((qu[b] & 1) ? kSegPar << b : 0) | (qu[b] > 0 ? kSegOld << b : 0);
+              ++qu[b];
+            }
+            if (!both) qn ^= 1;
+          }
           hand(PagedSeg{tb, te, flags, walk.keys, walk.tok0, walk.ntok, walk.pos0, walk.g,
                         walk.seq, {0, 0, 0}});
         }
@@ -618,14 +896,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_col = 128u * hd, o_col = 256u + 128u * hd;
     int sc = 0, oc[2] = {0, 0}, xc = 0;           // steps, accumulator uses, hand-overs
+    int kt = 0, fc = 0;                           // key tiles, few-row segments
     bool ok = true;
     for (int i = 0; ok; ++i) {
-      if (!warp_wait(bar_wfull(i % kPagedSegs), (i / kPagedSegs) & 1, wc)) break;
+      if (!warp_wait(bars.wfull(i % kPagedSegs), (i / kPagedSegs) & 1, wc)) break;
       // The segment stays in the ring until its end and is read again there:
       // its fields would not fit beside a row of scores in the registers.
       const volatile PagedSeg& sg = segs[i % kPagedSegs];
       const int te = sg.te, flags = sg.flags;
       if (te < 0) break;
+      if ((flags & kSegFew) && sg.keys > 0) {
+        const PagedSeg own{sg.tb, te, flags, sg.keys, sg.tok0, sg.ntok, sg.pos0, sg.g, sg.seq, {0, 0, 0}};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.wempty(i % kPagedSegs));
+        if (!(ok = few_segment<LIST>(a, own, smem, s_base, b0, wc, kt, fc++ & 1, oc[1]))) break;
+        kt += te - own.tb;
+        continue;
+      }
       const bool duo = (flags & kSegDuo) != 0;
       int t = sg.tb + (duo ? 0 : hd);
       const bool two = !duo && te - t > (hd ^ 1);  // both accumulators belong to these rows
@@ -643,31 +930,45 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       float m_used = -INFINITY, lsum = 0.f;
       bool started = false;
       for (; !none && t < te; t += duo ? 1 : 2) {
-        if (!(ok = warp_wait(bar_sfull(hd), sc & 1, wc))) break;
+        if (!(ok = warp_wait(bars.sfull(hd), sc & 1, wc))) break;
         ++sc;
         tc_fence_after();
         if (busy) {
           const int limit = min(128, seen - 128 * t);
-          uint32_t sr[4][32];
+          // The maximum first, 32 columns at a time; columns 0-63 stay in the
+          // registers, 64-127 are read again for the exponentials (two TMEM
+          // loads cost less than the spills of a whole row).
+          uint32_t sr[2][32], sx[32];
+          float mxv[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(tmem + lane_off + s_col + 32u * q, sr[q]);
-          tmem_ld_wait();
-          if (limit < 128) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
+          for (int u = 0; u < 4; ++u) mxv[u] = -INFINITY;
+          auto cut = [&](uint32_t(&x)[32], int q) {
+            if (limit < 32 * q + 32) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (32 * q + e >= limit) sr[q][e] = 0xff800000u;
-          }
-          float mxv[8];
+                if (32 * q + e >= limit) x[e] = 0xff800000u;
+            }
+          };
+          auto most = [&](const uint32_t(&x)[32]) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) mxv[u] = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mxv[e & 7] = fmaxf(mxv[e & 7], __uint_as_float(sr[q][e]));
-          const float mx2 = fmaxf(fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])),
-                                  fmaxf(fmaxf(mxv[4], mxv[5]), fmaxf(mxv[6], mxv[7]))) * a.sl2;
+            for (int e = 0; e < 32; ++e) mxv[e & 3] = fmaxf(mxv[e & 3], __uint_as_float(x[e]));
+          };
+          tmem_ld32(tmem + lane_off + s_col, sr[0]);
+          tmem_ld32(tmem + lane_off + s_col + 32u, sr[1]);
+          tmem_ld_wait();
+          tmem_ld32(tmem + lane_off + s_col + 64u, sx);
+          cut(sr[0], 0);
+          cut(sr[1], 1);
+          most(sr[0]);
+          most(sr[1]);
+          tmem_ld_wait();
+          cut(sx, 2);
+          most(sx);
+          tmem_ld32(tmem + lane_off + s_col + 96u, sx);
+          tmem_ld_wait();
+          cut(sx, 3);
+          most(sx);
+          const float mx2 = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])) * a.sl2;
           // the maximum in use may lag by up to 2^8 before O is rescaled
           const bool grow = mx2 > m_used + 8.0f;
           if (!started) {
@@ -692,34 +993,42 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           }
           started = true;
           const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
-          float ps[8];
+          float ps[4];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) ps[u] = 0.f;
+          for (int u = 0; u < 4; ++u) ps[u] = 0.f;
+          auto exps = [&](uint32_t(&x)[32]) {        // packed into the first 16
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-              const int q = 2 * h2 + cc;
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float p0 = fast_exp2(fmaf(__uint_as_float(sr[q][e]), a.sl2, neg_m));
-                const float p1 = fast_exp2(fmaf(__uint_as_float(sr[q][e + 1]), a.sl2, neg_m));
-                ps[(e >> 1) & 7] += p0 + p1;
-                sr[q][e >> 1] = pack_bf16x2(p0, p1);
-              }
+            for (int e = 0; e < 32; e += 2) {
+              const float p0 = fast_exp2(fmaf(__uint_as_float(x[e]), a.sl2, neg_m));
+              const float p1 = fast_exp2(fmaf(__uint_as_float(x[e + 1]), a.sl2, neg_m));
+              ps[(e >> 1) & 3] += p0 + p1;
+              x[e >> 1] = pack_bf16x2(p0, p1);
             }
-            tmem_st32_halves(tmem + lane_off + s_col + 32u * h2, sr[2 * h2], sr[2 * h2 + 1]);
-          }
-          lsum += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+          };
+          // columns 64-127 lie behind P's 64 and are still whole
+          tmem_ld32(tmem + lane_off + s_col + 64u, sx);
+          exps(sr[0]);
+          exps(sr[1]);
+          tmem_ld_wait();
+          tmem_st32_halves(tmem + lane_off + s_col, sr[0], sr[1]);
+          tmem_ld32(tmem + lane_off + s_col + 96u, sr[1]);
+          cut(sx, 2);
+          exps(sx);
+          tmem_ld_wait();
+          cut(sr[1], 3);
+          exps(sr[1]);
+          tmem_st32_halves(tmem + lane_off + s_col + 32u, sx, sr[1]);
+          lsum += (ps[0] + ps[1]) + (ps[2] + ps[3]);
           tmem_st_wait();
         }
         tc_fence_before();
-        mbar_arrive(bar_pfull(hd));
+        mbar_arrive(bars.pfull(hd));
       }
       if (!ok) break;
       // ----------------------------------------------------- segment's end
       const int use0 = oc[0], use1 = oc[1];
       if (!none) {
+        kt += te - sg.tb;
         ++oc[0];
         if (duo || two) ++oc[1];
       }
@@ -729,7 +1038,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       const long long tok = static_cast<long long>(sg.tok0) + ti;
       const int head = sg.g * a.group + (row - rt * a.group);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_wempty(i % kPagedSegs));
+      if (lane == 0) mbar_arrive(bars.wempty(i % kPagedSegs));
       if (none) {
         if (valid_row && (duo || hd == 0)) {
           uint4* dst = reinterpret_cast<uint4*>(a.o.at(0, tok, head));
@@ -738,20 +1047,30 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         continue;
       }
+      // Warpgroup 1 waits for accumulator 0 too, and its arrival frees it with
+      // warpgroup 0's: all loads of the segment have landed then, and it has not
+      // skipped a phase of the barriers it waits on when rows are few.
       if (!duo && hd == 1) {
-        if (!two) continue;
-        // hand (m, l) to warpgroup 0, which joins the two accumulators; it has
-        // read the last pair once it has freed the second accumulator
-        if (use1 > 0 && !(ok = warp_wait(bar_ofree(1), (use1 - 1) & 1, wc))) break;
-        ml[row] = m_used;
-        ml[128 + row] = lsum;
-        mbar_arrive(bar_xch);
-        if (!(ok = warp_wait(bar_odone(1), use1 & 1, wc))) break;
+        if (two) {
+          // hand (m, l) to warpgroup 0, which joins the two accumulators; it has
+          // read the last pair once it has freed the second accumulator
+          if (use1 > 0 && !(ok = warp_wait(bars.ofree(1), (use1 - 1) & 1, wc))) break;
+          ml[row] = m_used;
+          ml[128 + row] = lsum;
+          mbar_arrive(bars.xch());
+          if (!(ok = warp_wait(bars.odone(1), use1 & 1, wc))) break;
+        }
+        if (!(ok = warp_wait(bars.odone(0), use0 & 1, wc))) break;
+        mbar_arrive(bars.ofree(0));
         continue;
       }
-      if (two && !(ok = warp_wait(bar_xch, xc++ & 1, wc))) break;
-      if (!(ok = warp_wait(bar_odone(hd), (hd ? use1 : use0) & 1, wc))) break;
-      if (two && !(ok = warp_wait(bar_odone(1), use1 & 1, wc))) break;
+      if (two && !(ok = warp_wait(bars.xch(), xc++ & 1, wc))) break;
+      if (!(ok = warp_wait(bars.odone(0), use0 & 1, wc))) break;
+      if (hd == 1) {
+        mbar_arrive(bars.ofree(0));
+        if (!(ok = warp_wait(bars.odone(1), use1 & 1, wc))) break;
+      }
+      if (two && !(ok = warp_wait(bars.odone(1), use1 & 1, wc))) break;
       tc_fence_after();
       float* part = a.part + (2LL * c + ((flags & kSegStart) ? 1 : 0)) * kPagedSlotFloats;
       const int prow = (duo ? hd * 128 : 0) + row;
@@ -818,8 +1137,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
       }
       tc_fence_before();
-      mbar_arrive(bar_ofree(hd));
-      if (two) mbar_arrive(bar_ofree(1));
+      mbar_arrive(bars.ofree(hd));
+      if (two) mbar_arrive(bars.ofree(1));
     }
   }
 

@@ -336,6 +336,17 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// D[16x8] += A[16x16] B[16x8], bf16 inputs, fp32 accumulation, operands in a
+// warp's registers: for the few rows that a 128-row tcgen05 tile would waste.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&x)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
+}
+
 // 2^x on the multi-function unit (PTX ex2.approx.ftz.f32); 2^-inf = +0.
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;

@@ -350,6 +350,7 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
   const int group = p->heads_q / p->heads_kv;
   PagedAttnArgs a;
   a.q = seqs_of(p, cu_q, kv_lens, block_table, error_word);
+  a.xq = rows_of(q);
   a.o = rows_of(o);
   a.lse = lse;
   a.lists = lists;

@@ -122,3 +122,19 @@ def test_own_lists():
     o, lse = attend(b, p, torch.from_numpy(lists).cuda(), torch.from_numpy(counts).cuda())
     check_attention(b, o, lse, pages_of=lambda t, g: want[(t, g)])
     b.ok()
+
+
+@pytest.mark.parametrize("hq,hkv,page,seed", [(4, 2, 16, 0), (20, 4, 32, 1), (8, 1, 64, 2),
+                                              (6, 6, 128, 3), (32, 1, 16, 4), (12, 2, 16, 5)])
+def test_batches_that_mix_tokens_and_chunks(hq, hkv, page, seed):
+    # few rows, one row tile and two, with tails of all of them, in any order
+    rng = np.random.default_rng(seed)
+    seqs = []
+    for _ in range(40):
+        n = int(rng.choice([0, 1, 1, 1, 2, 3, 5, 17, 26, 40, 65, 130]))
+        seqs.append((n, n + int(rng.choice([0, 0, 1, 100, 127, 128, 300, 700]))))
+    b = Batch(hq, hkv, page, seqs, seed=seed)
+    o, lse = attend(b)
+    rows = set(int(t) for t in np.random.default_rng(seed).permutation(b.T)[:60])
+    check_attention(b, o, lse, rows=rows | set(int(x) for x in b.cu[:-1]))
+    b.ok()
