@@ -42,12 +42,11 @@
 // result does not depend on timing.
 //
 // Rows of V past the last visible key of a tile (the unfilled end of a page,
-// pages not loaded) are cleared in shared memory by a warp of their own: their
-// probability is 0, but 0 * NaN is not.
+// pages not loaded) are cleared before they are read: their probability is 0,
+// but 0 * NaN is not.
 //
 // Roles (384 threads): warps 0-3 / 4-7 softmax of slot 0 / 1, warp 8 loads,
-// warp 9 MMA and TMEM, warp 10 clears the ends of V tiles, warp 11 walks the
-// CTA's piece and hands its segments to the others through a ring of four, so
+// warp 9 MMA, TMEM and the ends of V tiles, warp 10 walks the CTA's piece and hands its segments to the others through a ring of four, so
 // that the lengths and lists of the next units are read ahead.
 // TMEM columns: S_0 [0,128) (P_0 in [0,64)), S_1 [128,256), O_0 [256,384),
 // O_1 [384,512).
@@ -123,7 +122,9 @@ struct PagedAttnArgs {
   uint32_t debug;
 };
 
-// One partial slot: O [256 rows][128], m [256], l [256].
+// One partial slot: O [32 groups of four columns][256 rows][4], m [256], l [256]:
+// threads that own a row each store 512 contiguous bytes together, and four
+// rows by eight groups are whole sectors to the combine.
 constexpr int kPagedSlotRows = 256;
 constexpr long long kPagedSlotFloats = 130LL * kPagedSlotRows;
 
@@ -317,7 +318,7 @@ struct PagedBars {
   __device__ __forceinline__ uint32_t kempty(int s) const { return at(3 + s); }
   __device__ __forceinline__ uint32_t vfull(int s) const { return at(6 + s); }
   __device__ __forceinline__ uint32_t vempty(int s) const { return at(8 + s); }
-  __device__ __forceinline__ uint32_t vclean(int s) const { return at(10 + s); }
+  __device__ __forceinline__ uint32_t phalf(int h) const { return at(10 + h); }
   __device__ __forceinline__ uint32_t sfull(int h) const { return at(12 + h); }
   __device__ __forceinline__ uint32_t pfull(int h) const { return at(14 + h); }
   __device__ __forceinline__ uint32_t odone(int h) const { return at(16 + h); }
@@ -437,7 +438,6 @@ __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const PagedSeg 
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.kempty(ks_));
     if (!warp_wait(bars.vfull(vs_), (kt / kPagedVStages) & 1, wc)) return false;
-    if (!warp_wait(bars.vclean(vs_), (kt / kPagedVStages) & 1, wc)) return false;
     if (left > 0) {
       // matrix i: key half i % 2, 16-byte chunk i / 2 of a pair
       const int key = 16 * warp + (lane & 15);
@@ -447,6 +447,14 @@ __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const PagedSeg 
         const int chunk = (2 * j + (lane >> 4)) & 7;
         ldsm4_t(vf, (s_base + (2u + kPagedKStages + vs_) * kTileBytes) + (j >> 2) * kHalfBytes + key * 128u +
                         ((chunk ^ (key & 7)) << 4));
+        if (left < 16) {
+          // rows behind the last key: their probability is 0, but 0 * NaN is not
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k0 = c2 + 8 * (e & 1);
+            vf[e] &= k0 + 1 < left ? 0xffffffffu : k0 < left ? 0xffffu : 0u;
+          }
+        }
         mma_16816(acc[2 * j], pf, vf[0], vf[1]);
         mma_16816(acc[2 * j + 1], pf, vf[2], vf[3]);
       }
@@ -510,7 +518,7 @@ __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const PagedSeg 
         a.lse[tok * a.Hq + head] =
             ll > 0.f ? mm * 0.69314718055994531f + logf(ll) : -INFINITY;
     } else {
-      *reinterpret_cast<float4*>(part + rr * 128 + 4 * lane) = y;
+      *reinterpret_cast<float4*>(part + (lane * kPagedSlotRows + rr) * 4) = y;
       if (lane == 0) {
         part[128 * kPagedSlotRows + rr] = mm;
         part[129 * kPagedSlotRows + rr] = ll;
@@ -558,22 +566,22 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     for (int i = 0; i < kPagedVStages; ++i) {
       mbar_init(bars.vfull(i), 1);
       mbar_init(bars.vempty(i), kReaders);
-      mbar_init(bars.vclean(i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars.sfull(i), 1);
-      mbar_init(bars.pfull(i), 128);
+      mbar_init(bars.phalf(i), 4);        // warps, by one lane each
+      mbar_init(bars.pfull(i), 4);
       mbar_init(bars.odone(i), 1);
-      mbar_init(bars.ofree(i), i == 0 ? 256 : 128);
+      mbar_init(bars.ofree(i), i == 0 ? 8 : 4);
       mbar_init(bars.qfull(i), 1);
       mbar_init(bars.qfree(i), kReaders);
     }
     for (int i = 0; i < kPagedSegs; ++i) {
       mbar_init(bars.wfull(i), 1);
-      mbar_init(bars.wempty(i), 11);     // loads, MMA, clearing, eight softmax warps
+      mbar_init(bars.wempty(i), 10);     // loads, MMA, eight softmax warps
     }
     mbar_init(bars.few(), 8);
-    mbar_init(bars.xch(), 128);
+    mbar_init(bars.xch(), 4);
     mbar_init(bars.drain(), 1);
     mbar_init(bars.stall(), 1);
     *abort_flag = 0u;
@@ -618,7 +626,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
   const WaitCtx wc{abort_flag, a.q.err, a.wait_ns};
   // Segment i of the piece, copied out of the ring; false at its end.
   auto take = [&](int i, PagedSeg& sg) -> bool {
@@ -631,7 +639,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
   };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
     if (warp == 8) {
       // ----------------------------------------------------------- loads
       const int ppt = 128 >> a.q.shift;             // pages per tile
@@ -731,7 +739,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       // ------------------------------------------------------- MMA issuer
       bool ok = true;
       if (a.debug & 1u) ok = warp_wait(bars.stall(), 0, wc);   // never signalled: test hook
-      int kt = 0, pc[2] = {0, 0}, oc[2] = {0, 0};
+      int kt = 0, pc0 = 0, pc1 = 0, oc0 = 0, oc1 = 0;
       auto commit_all = [](uint32_t bar) {
         mbar_arrive_n(bar, kReaders - 1);
         mma_commit(bar);
@@ -756,92 +764,100 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           }
           continue;
         }
-        if (lane == 0) {
-          const int duo = (sg.flags & kSegDuo) ? 1 : 0;
-          const int tiles = sg.te - sg.tb, steps = tiles << duo;
-          const int buf = (sg.flags & kSegBuf) ? 1 : 0;
-          auto qk = [&](int j) -> bool {
-            const int h = j & 1, k = kt + (j >> duo), st = k % kPagedKStages;
-            const int qb = duo ? h : buf;
-            if (j < 2 && (duo || j == 0)) {
-              if (!mbar_wait(bars.qfull(qb), (sg.flags & (kSegPar << qb)) ? 1 : 0, wc)) return false;
-            }
-            if (!mbar_wait(bars.kfull(st), (k / kPagedKStages) & 1, wc)) return false;
-            tc_fence_after();
+        // Everything an MMA is told is the same in all lanes, and the compiler
+        // has to see that (broadcasts from lane 0): descriptors then stay in
+        // uniform registers.  Computed by the issuing lane alone they cost some
+        // 150 cycles per MMA, more than the MMA itself.
+        const int flags = __shfl_sync(0xffffffffu, sg.flags, 0);
+        const int tiles = __shfl_sync(0xffffffffu, sg.te - sg.tb, 0);
+        const int kt0 = __shfl_sync(0xffffffffu, kt, 0);
+        const int duo = (flags & kSegDuo) ? 1 : 0;
+        const int steps = tiles << duo;
+        const int buf = (flags & kSegBuf) ? 1 : 0;
+        auto qk = [&](int j) -> bool {
+          const int h = j & 1, k = kt0 + (j >> duo), st = k % kPagedKStages;
+          const int qb = duo ? h : buf;
+          if (j < 2 && (duo || j == 0)) {
+            if (!warp_wait(bars.qfull(qb), (flags & (kSegPar << qb)) ? 1 : 0, wc)) return false;
+          }
+          if (!warp_wait(bars.kfull(st), (k / kPagedKStages) & 1, wc)) return false;
+          tc_fence_after();
+          const uint64_t qd = smem_desc_sw128(s_q(qb), 16), kd = smem_desc_sw128(s_k(st), 16);
+          const uint32_t d = tmem + 128u * h;
+          if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
-              const uint32_t off = (ks >> 2) * kHalfBytes + (ks & 3) * 32u;
-              mma_bf16_ss(tmem + 128u * h, smem_desc_sw128(s_q(qb) + off, 16),
-                          smem_desc_sw128(s_k(st) + off, 16), kIdescQK, ks > 0 ? 1u : 0u);
+              const uint64_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32u) >> 4;
+              mma_bf16_ss(d, qd + off, kd + off, kIdescQK, ks > 0 ? 1u : 0u);
             }
             mma_commit(bars.sfull(h));
             if (!duo || h == 1) commit_all(bars.kempty(st));
             if (j + 1 + duo >= steps) commit_all(bars.qfree(qb));
-            return true;
-          };
-          auto pv = [&](int j) -> bool {
-            const int h = j & 1, k = kt + (j >> duo), st = k % kPagedVStages;
-            const bool first = j < 2;
-            if (!mbar_wait(bars.pfull(h), pc[h] & 1, wc)) return false;
-            ++pc[h];
-            if (!mbar_wait(bars.vfull(st), (k / kPagedVStages) & 1, wc)) return false;
-            if (!mbar_wait(bars.vclean(st), (k / kPagedVStages) & 1, wc)) return false;
-            if (first) {
-              // this accumulator of the segment before has been read
-              if (oc[h] > 0 && !mbar_wait(bars.ofree(h), (oc[h] - 1) & 1, wc)) return false;
-              ++oc[h];
+          }
+          __syncwarp();
+          return true;
+        };
+        auto pv = [&](int j) -> bool {
+          const int h = j & 1, k = kt0 + (j >> duo), st = k % kPagedVStages;
+          const bool first = j < 2;
+          const int uses_p = (h ? pc1 : pc0)++;
+          if (!warp_wait(bars.vfull(st), (k / kPagedVStages) & 1, wc)) return false;
+          const int valid = sg.keys - 128 * (sg.tb + (j >> duo));
+          if (valid < 128 && (!duo || h == 0)) {
+            // zeros behind the last V row: whole 128-byte rows, so the swizzle
+            // within a row does not matter
+            uint8_t* tile = smem + (2 + kPagedKStages + st) * kTileBytes;
+            for (int x = valid * 8 + lane; x < 128 * 8; x += 32) {
+              reinterpret_cast<uint4*>(tile)[x] = make_uint4(0, 0, 0, 0);
+              reinterpret_cast<uint4*>(tile + kHalfBytes)[x] = make_uint4(0, 0, 0, 0);
             }
-            tc_fence_after();
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (first) {
+            // this accumulator of the segment before has been read
+            int& uses = h ? oc1 : oc0;
+            if (uses > 0 && !warp_wait(bars.ofree(h), (uses - 1) & 1, wc)) return false;
+            ++uses;
+          }
+          const uint64_t vd = smem_desc_sw128(s_v(st), kHalfBytes);
+          const uint32_t d = tmem + 256u + 128u * h, p = tmem + 128u * h;
+          if (!warp_wait(bars.phalf(h), uses_p & 1, wc)) return false;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              mma_bf16_ts(tmem + 256u + 128u * h, tmem + 128u * h + 8u * ks,
-                          smem_desc_sw128(s_v(st) + ks * 2048u, kHalfBytes), kIdescPV,
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ts(d, p + 8u * ks, vd + ks * (2048u >> 4), kIdescPV,
                           (!first || ks > 0) ? 1u : 0u);
-            }
+          }
+          __syncwarp();
+          if (!warp_wait(bars.pfull(h), uses_p & 1, wc)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 4; ks < 8; ++ks)
+              mma_bf16_ts(d, p + 8u * ks, vd + ks * (2048u >> 4), kIdescPV, 1u);
             if (!duo || h == 1) commit_all(bars.vempty(st));
             if (j + 2 >= steps) mma_commit(bars.odone(h));
-            return true;
-          };
-          for (int j = 0; ok && j < 2 && j < steps; ++j) ok = qk(j);
-          for (int j = 0; ok && j < steps; ++j) {
-            ok = pv(j);
-            if (ok && j + 2 < steps) ok = qk(j + 2);
           }
+          __syncwarp();
+          return true;
+        };
+        for (int j = 0; ok && j < 2 && j < steps; ++j) ok = qk(j);
+        for (int j = 0; ok && j < steps; ++j) {
+          ok = pv(j);
+          if (ok && j + 2 < steps) ok = qk(j + 2);
         }
-        kt += sg.te - sg.tb;
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        kt += tiles;
       }
-      // every MMA issued by this thread has completed once this arrives
-      if (lane == 0) {
+      // every MMA issued by this warp's elected lane has completed once this
+      // arrives (elect.sync picks the same lane each time)
+      if (elect_one()) {
         mma_commit(bars.drain());
         mbar_drain(bars.drain(), 0, a.wait_ns);
       }
       __syncwarp();
-    } else if (warp == 10) {
-      // ------------------------------------- zeros behind the last V rows
-      int kt = 0;
-      bool ok = true;
-      PagedSeg sg;
-      for (int i = 0; ok && take(i, sg); ++i) {
-        if (sg.keys == 0) continue;
-        for (int t = sg.tb; t < sg.te; ++t, ++kt) {
-          const int st = kt % kPagedVStages;
-          if (!(ok = warp_wait(bars.vfull(st), (kt / kPagedVStages) & 1, wc))) break;
-          const int valid = sg.keys - 128 * t;
-          if (valid < 128) {
-            // whole 128-byte rows, so the swizzle within a row does not matter
-            uint8_t* tile = smem + (2 + kPagedKStages + st) * kTileBytes;
-            for (int i = valid * 8 + lane; i < 128 * 8; i += 32) {
-              reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
-              reinterpret_cast<uint4*>(tile + kHalfBytes)[i] = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars.vclean(st));
-        }
-      }
-    } else if (lane == 0) {
+    } else if (warp == 10 && lane == 0) {
       // ----------------------------------------------- the CTA's segments
       PagedWalk<LIST> walk(a);
       walk.x0 = f.total * c / G;
@@ -852,8 +868,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       bool ok = true;
       auto hand = [&](const PagedSeg& sg) {
         const int r = i % kPagedSegs;
-        if (i >= kPagedSegs && !(ok = mbar_wait(bars.wempty(r), (i / kPagedSegs - 1) & 1, wc)))
-          return;
+        if (i >= kPagedSegs) {
+          // a long wait as a rule: the warp sleeps in between, out of the others' way
+          const uint32_t parity = (i / kPagedSegs - 1) & 1;
+          for (int k = 0; k < 64 && !mbar_try_wait(bars.wempty(r), parity); ++k) __nanosleep(500);
+          if (!(ok = mbar_wait(bars.wempty(r), parity, wc))) return;
+        }
         segs[r] = sg;
         mbar_arrive(bars.wfull(r));
         ++i;
@@ -890,11 +910,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     }
   } else {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
     const int hd = warp >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_col = 128u * hd, o_col = 256u + 128u * hd;
+    // a warp's TMEM and shared-memory accesses so far, then one arrival
+    auto warp_arrive = [&](uint32_t bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     int sc = 0, oc[2] = {0, 0}, xc = 0;           // steps, accumulator uses, hand-overs
     int kt = 0, fc = 0;                           // key tiles, few-row segments
     bool ok = true;
@@ -935,40 +961,27 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         tc_fence_after();
         if (busy) {
           const int limit = min(128, seen - 128 * t);
-          // The maximum first, 32 columns at a time; columns 0-63 stay in the
-          // registers, 64-127 are read again for the exponentials (two TMEM
-          // loads cost less than the spills of a whole row).
-          uint32_t sr[2][32], sx[32];
-          float mxv[4];
+          uint32_t sr[4][32];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mxv[u] = -INFINITY;
-          auto cut = [&](uint32_t(&x)[32], int q) {
-            if (limit < 32 * q + 32) {
+          for (int q = 0; q < 4; ++q) tmem_ld32(tmem + lane_off + s_col + 32u * q, sr[q]);
+          tmem_ld_wait();
+          if (limit < 128) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (32 * q + e >= limit) x[e] = 0xff800000u;
-            }
-          };
-          auto most = [&](const uint32_t(&x)[32]) {
+                if (32 * q + e >= limit) sr[q][e] = 0xff800000u;
+          }
+          float mxv[8];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mxv[e & 3] = fmaxf(mxv[e & 3], __uint_as_float(x[e]));
-          };
-          tmem_ld32(tmem + lane_off + s_col, sr[0]);
-          tmem_ld32(tmem + lane_off + s_col + 32u, sr[1]);
-          tmem_ld_wait();
-          tmem_ld32(tmem + lane_off + s_col + 64u, sx);
-          cut(sr[0], 0);
-          cut(sr[1], 1);
-          most(sr[0]);
-          most(sr[1]);
-          tmem_ld_wait();
-          cut(sx, 2);
-          most(sx);
-          tmem_ld32(tmem + lane_off + s_col + 96u, sx);
-          tmem_ld_wait();
-          cut(sx, 3);
-          most(sx);
-          const float mx2 = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])) * a.sl2;
+          for (int u = 0; u < 8; ++u)
+            mxv[u] = fmaxf(__uint_as_float(sr[0][2 * u]), __uint_as_float(sr[0][2 * u + 1]));
+#pragma unroll
+          for (int e = 16; e < 128; e += 2)
+            mxv[(e >> 1) & 7] = max3(mxv[(e >> 1) & 7], __uint_as_float(sr[e >> 5][e & 31]),
+                                     __uint_as_float(sr[e >> 5][(e & 31) + 1]));
+          const float mx2 = max3(max3(mxv[0], mxv[1], mxv[2]), max3(mxv[3], mxv[4], mxv[5]),
+                                 fmaxf(mxv[6], mxv[7])) * a.sl2;
           // the maximum in use may lag by up to 2^8 before O is rescaled
           const bool grow = mx2 > m_used + 8.0f;
           if (!started) {
@@ -993,36 +1006,36 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           }
           started = true;
           const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
-          float ps[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) ps[u] = 0.f;
+          const uint64_t scale2 = pack_f32x2(a.sl2, a.sl2), neg2 = pack_f32x2(neg_m, neg_m);
+          uint64_t ps[2] = {0ull, 0ull};
           auto exps = [&](uint32_t(&x)[32]) {        // packed into the first 16
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float p0 = fast_exp2(fmaf(__uint_as_float(x[e]), a.sl2, neg_m));
-              const float p1 = fast_exp2(fmaf(__uint_as_float(x[e + 1]), a.sl2, neg_m));
-              ps[(e >> 1) & 3] += p0 + p1;
+              float p0, p1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                     scale2, neg2), p0, p1);
+              p0 = fast_exp2(p0);
+              p1 = fast_exp2(p1);
+              ps[(e >> 1) & 1] = add_f32x2(ps[(e >> 1) & 1], pack_f32x2(p0, p1));
               x[e >> 1] = pack_bf16x2(p0, p1);
             }
           };
-          // columns 64-127 lie behind P's 64 and are still whole
-          tmem_ld32(tmem + lane_off + s_col + 64u, sx);
           exps(sr[0]);
           exps(sr[1]);
-          tmem_ld_wait();
           tmem_st32_halves(tmem + lane_off + s_col, sr[0], sr[1]);
-          tmem_ld32(tmem + lane_off + s_col + 96u, sr[1]);
-          cut(sx, 2);
-          exps(sx);
-          tmem_ld_wait();
-          cut(sr[1], 3);
-          exps(sr[1]);
-          tmem_st32_halves(tmem + lane_off + s_col + 32u, sx, sr[1]);
-          lsum += (ps[0] + ps[1]) + (ps[2] + ps[3]);
           tmem_st_wait();
+          warp_arrive(bars.phalf(hd));               // PV over the first 64 keys may begin
+          exps(sr[2]);
+          exps(sr[3]);
+          tmem_st32_halves(tmem + lane_off + s_col + 32u, sr[2], sr[3]);
+          float l0, l1;
+          unpack_f32x2(add_f32x2(ps[0], ps[1]), l0, l1);
+          lsum += l0 + l1;
+          tmem_st_wait();
+        } else {
+          warp_arrive(bars.phalf(hd));
         }
-        tc_fence_before();
-        mbar_arrive(bars.pfull(hd));
+        warp_arrive(bars.pfull(hd));
       }
       if (!ok) break;
       // ----------------------------------------------------- segment's end
@@ -1034,9 +1047,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       }
       const bool whole = (flags & kSegWhole) != 0;
       const int rt = row / a.group, ti = rt + (duo ? hd * a.tpt1 : 0);
-      const bool valid_row = rt < a.tpt1 && ti < sg.ntok;
-      const long long tok = static_cast<long long>(sg.tok0) + ti;
-      const int head = sg.g * a.group + (row - rt * a.group);
+      const int tok0 = sg.tok0, ntok = sg.ntok, g0 = sg.g * a.group;
+      const bool valid_row = rt < a.tpt1 && ti < ntok;
+      const long long tok = static_cast<long long>(tok0) + ti;
+      const int head = g0 + (row - rt * a.group);
       __syncwarp();
       if (lane == 0) mbar_arrive(bars.wempty(i % kPagedSegs));
       if (none) {
@@ -1057,17 +1071,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           if (use1 > 0 && !(ok = warp_wait(bars.ofree(1), (use1 - 1) & 1, wc))) break;
           ml[row] = m_used;
           ml[128 + row] = lsum;
-          mbar_arrive(bars.xch());
+          warp_arrive(bars.xch());
           if (!(ok = warp_wait(bars.odone(1), use1 & 1, wc))) break;
         }
         if (!(ok = warp_wait(bars.odone(0), use0 & 1, wc))) break;
-        mbar_arrive(bars.ofree(0));
+        warp_arrive(bars.ofree(0));
         continue;
       }
       if (two && !(ok = warp_wait(bars.xch(), xc++ & 1, wc))) break;
       if (!(ok = warp_wait(bars.odone(0), use0 & 1, wc))) break;
       if (hd == 1) {
-        mbar_arrive(bars.ofree(0));
+        warp_arrive(bars.ofree(0));
         if (!(ok = warp_wait(bars.odone(1), use1 & 1, wc))) break;
       }
       if (two && !(ok = warp_wait(bars.odone(1), use1 & 1, wc))) break;
@@ -1087,6 +1101,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       fac0 *= inv;
       fac1 *= inv;
       if (busy) {
+        // rows of this lane's four, when stored: null behind the last
+        __nv_bfloat16* dst[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rk = quad * 32 + (lane & ~3) + k, rkt = rk / a.group;
+          const int tk = rkt + (duo ? hd * a.tpt1 : 0);
+          dst[k] = rkt < a.tpt1 && tk < ntok
+                       ? a.o.at(0, static_cast<long long>(tok0) + tk, g0 + (rk - rkt * a.group))
+                       : nullptr;
+        }
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           uint32_t ov[32];
@@ -1105,25 +1129,47 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
               ov[e] = __float_as_uint(
                   l > 0.f ? fmaf(__uint_as_float(ow[e]), fac1, __uint_as_float(ov[e])) : 0.f);
           }
-          if (valid_row) {
-            if (whole) {
-              uint4* dst = reinterpret_cast<uint4*>(a.o.at(0, tok, head) + 32 * q);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t* x = ov + 8 * i;
-                dst[i] = make_uint4(
-                    pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                    pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                    pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
-                    pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
-              }
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(part + prow * 128 + 32 * q);
+          if (!whole) {
+            if (valid_row) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+                *reinterpret_cast<uint4*>(part + ((8 * q + i) * kPagedSlotRows + prow) * 4) =
+                    make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+            }
+            continue;
+          }
+          // Four lanes exchange the 16-byte quarters of their rows' 64 bytes, so
+          // that a store covers eight rows of 64 bytes instead of 32 of 16.
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t* y = ov + 8 * i;
+            x[i] = make_uint4(pack_bf16x2(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                              pack_bf16x2(__uint_as_float(y[2]), __uint_as_float(y[3])),
+                              pack_bf16x2(__uint_as_float(y[4]), __uint_as_float(y[5])),
+                              pack_bf16x2(__uint_as_float(y[6]), __uint_as_float(y[7])));
+          }
+#pragma unroll
+          for (int st = 1; st <= 2; ++st) {
+            const bool up = (lane & st) != 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int lo = st == 1 ? 2 * k : k, hi = lo + st;
+              uint4 z = up ? x[lo] : x[hi];
+              z.x = __shfl_xor_sync(0xffffffffu, z.x, st);
+              z.y = __shfl_xor_sync(0xffffffffu, z.y, st);
+              z.z = __shfl_xor_sync(0xffffffffu, z.z, st);
+              z.w = __shfl_xor_sync(0xffffffffu, z.w, st);
+              if (up)
+                x[lo] = z;
+              else
+                x[hi] = z;
             }
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (dst[k] != nullptr)
+              *reinterpret_cast<uint4*>(dst[k] + 32 * q + 8 * (lane & 3)) = x[k];
         }
         if (valid_row) {
           if (whole) {
@@ -1136,9 +1182,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           }
         }
       }
-      tc_fence_before();
-      mbar_arrive(bars.ofree(hd));
-      if (two) mbar_arrive(bars.ofree(1));
+      warp_arrive(bars.ofree(hd));
+      if (two) warp_arrive(bars.ofree(1));
     }
   }
 
@@ -1150,70 +1195,76 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 // Joins the pieces of every unit that several CTAs share: blocks x look at the
 // record of CTA x.  O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.  A warp
-// per row: the lanes read the pieces' (m, l) side by side and turn them into
-// weights, then each lane sums four columns over the pieces, all loads
-// independent (a serial merge took 17 us for 8 pieces of one token).
+// has four rows by 32 columns: its lanes read the pieces' (m, l) side by side
+// and leave the weights in shared memory, then each lane sums four columns of
+// a row over the pieces, all loads independent (a serial merge took 17 us for
+// 8 pieces of one token).
 constexpr int kCombineThreads = 256;
+constexpr int kPagedMaxCtas = 160;
 
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedAttnArgs a) {
+  __shared__ float weights[kCombineThreads / 32][4][kPagedMaxCtas];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedRecord rec = a.rec[blockIdx.x];
   if (rec.c1 < 0) return;
-  const int c0 = blockIdx.x, np = rec.c1 - c0 + 1;
-  const int lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x, np = min(rec.c1 - c0 + 1, kPagedMaxCtas);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = rec.ntok * a.group;
-  const int stride = gridDim.y * (kCombineThreads / 32);
+  const int items = (rows + 3) / 4 * 4;            // row quads x four column blocks
   // slot of piece i: the first CTA's is its second
   auto slot = [&](int i) {
     return a.part + (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * kPagedSlotFloats;
   };
-  for (int i = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5); i < rows; i += stride) {
+  for (int it = blockIdx.y * (kCombineThreads / 32) + warp; it < items;
+       it += gridDim.y * (kCombineThreads / 32)) {
+    const int r = lane & 3, cg = lane >> 2;
+    const int i = min((it >> 2) * 4 + r, rows - 1);
+    const bool on = (it >> 2) * 4 + r < rows;
     const int ti = i / a.group, hh = i - ti * a.group;
     const int tile = ti >= a.tpt1 ? 1 : 0;
     const int prow = tile * 128 + (ti - tile * a.tpt1) * a.group + hh;
-    constexpr int kGroups = 5;                     // of 32 pieces: up to 160 CTAs
-    float mw[kGroups], lw[kGroups], m = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-      const int p = 32 * k + lane;
-      mw[k] = p < np ? slot(p)[128 * kPagedSlotRows + prow] : -INFINITY;
-      lw[k] = p < np ? slot(p)[129 * kPagedSlotRows + prow] : 0.f;
-      m = fmaxf(m, mw[k]);
+    float m = -INFINITY;
+    __syncwarp();
+    for (int p = cg; p < np; p += 8) {
+      const float x = slot(p)[128 * kPagedSlotRows + prow];
+      weights[warp][r][p] = x;
+      m = fmaxf(m, x);
     }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f;
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-      mw[k] = mw[k] == -INFINITY ? 0.f : exp2f(mw[k] - m);
-      l = fmaf(lw[k], mw[k], l);
+    for (int p = cg; p < np; p += 8) {
+      const float x = weights[warp][r][p];
+      const float w = x == -INFINITY ? 0.f : exp2f(x - m);
+      weights[warp][r][p] = w;
+      l = fmaf(slot(p)[129 * kPagedSlotRows + prow], w, l);
     }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    __syncwarp();
+    const int c4 = 8 * (it & 3) + cg;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-      const int n = min(32, np - 32 * k);
 #pragma unroll 8
-      for (int p = 0; p < n; ++p) {
-        const float wgt = __shfl_sync(0xffffffffu, mw[k], p);
-        const float4 x =
-            *reinterpret_cast<const float4*>(slot(32 * k + p) + prow * 128 + 4 * lane);
-        acc.x = fmaf(x.x, wgt, acc.x);
-        acc.y = fmaf(x.y, wgt, acc.y);
-        acc.z = fmaf(x.z, wgt, acc.z);
-        acc.w = fmaf(x.w, wgt, acc.w);
-      }
+    for (int p = 0; p < np; ++p) {
+      const float w = weights[warp][r][p];
+      const float4 x =
+          *reinterpret_cast<const float4*>(slot(p) + (c4 * kPagedSlotRows + prow) * 4);
+      acc.x = fmaf(x.x, w, acc.x);
+      acc.y = fmaf(x.y, w, acc.y);
+      acc.z = fmaf(x.z, w, acc.z);
+      acc.w = fmaf(x.w, w, acc.w);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const long long tok = static_cast<long long>(rec.tok0) + ti;
-    const int head = rec.g * a.group + hh;
-    uint2 y;
-    y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-    y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(a.o.at(0, tok, head) + 4 * lane) = y;
-    if (a.lse && lane == 0)
-      a.lse[tok * a.Hq + head] = l > 0.f ? m * 0.69314718055994531f + logf(l) : -INFINITY;
+    if (on) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const long long tok = static_cast<long long>(rec.tok0) + ti;
+      const int head = rec.g * a.group + hh;
+      uint2 y;
+      y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+      y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(a.o.at(0, tok, head) + 4 * c4) = y;
+      if (a.lse && c4 == 0)
+        a.lse[tok * a.Hq + head] = l > 0.f ? m * 0.69314718055994531f + logf(l) : -INFINITY;
+    }
   }
 }
 

@@ -20,6 +20,7 @@ using namespace spa;
 
 // CTAs of the attention: one per SM of the chip's 148.
 constexpr int kPagedGrid = 148;
+static_assert(kPagedGrid <= kPagedMaxCtas, "weights of the combine");
 
 bool rows_ok(const spa_rows* r) {
   return r && r->data && aligned16(r->data) && r->stride_batch % 8 == 0 &&
@@ -377,7 +378,8 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
       !map_2d(&tk, kBF16, 2, k_cache, 128, cache_rows, 64, p->page_size, kSW128) ||
       !map_2d(&tv, kBF16, 2, v_cache, 128, cache_rows, 64, p->page_size, kSW128))
     return SPA_ERR_CUDA;
-  // combine blocks beside one another: a warp per row of a usual unit
+  // combine blocks beside one another: a warp per row of a usual unit (four
+  // rows by a quarter of the columns)
   long long rows = lists ? group : (long long)p->tokens * group / p->seqs;
   if (rows > kPagedSlotRows) rows = kPagedSlotRows;
   const int cy = rows > 8 ? (int)(rows + 7) / 8 : 1;
