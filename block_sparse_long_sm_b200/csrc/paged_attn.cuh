@@ -33,8 +33,7 @@
 // A step batch that mixes prompt chunks and single tokens has both.
 //
 // Work split.  All (sequence, kv head, row tiles) units lie end to end on one
-// line, a key tile being one step long (two with two row tiles: twice the
-// products), and each CTA (one per SM, persistent) takes an equal piece of
+// line, as long as they take, and each CTA (one per SM, persistent) takes an equal piece of
 // that line, found by a scan over the sequences' lengths: every SM has the same
 // work however ragged the batch is, one long sequence included.  A unit that one CTA covers is finished there; the pieces
 // of the others (at most two per CTA) go to the workspace in fp32 and
@@ -103,6 +102,12 @@ constexpr int kFewRows = 16;
 // Arrivals that free a K, V or Q buffer: of the eight softmax warps and the MMA
 // warp when rows are few, else of the MMA's commit, which counts for all.
 constexpr uint32_t kReaders = 9;
+// Lengths on the line of work, in units of about 0.55 us: a key tile (64 KB of K
+// and V from memory: 1.6 us; with two row tiles 2.2 us of products), and what a
+// unit costs beside its tiles (Q, the first tile's way through, joining and
+// storing: measured 2 us for few rows, 6 us for row tiles).
+constexpr int kTileOne = 3, kTileDuo = 4, kEdgeFew = 4, kEdgeRows = 11;
+static_assert(kTileDuo > kTileOne, "tells two row tiles");
 
 struct PagedAttnArgs {
   Seqs q;
@@ -111,7 +116,7 @@ struct PagedAttnArgs {
   const int32_t* lists;      // [T][Hkv][width] or null
   const int32_t* counts;     // [T][Hkv]
   int width;                 // list entries per (token, kv head)
-  int wu;                    // key tiles of a full list
+  int unit_length;           // length on the line of a full list
   int Hq, Hkv, group;
   int tpt1;                  // tokens per 128-row tile
   int pitch;                 // 128-element rows between pages
@@ -146,7 +151,7 @@ struct PagedWalk {
   int nr;                    // its row tiles
   // the current unit
   int seq, tok0, ntok, pos0, keys, nt;
-  int w, flat;               // length of one of its tiles on the line, of all
+  int w, edge, flat;         // lengths on the line: a tile, what precedes them, all
 
   __device__ __forceinline__ explicit PagedWalk(const PagedAttnArgs& args) : a(args) {}
 
@@ -157,9 +162,16 @@ struct PagedWalk {
     return max(0, pos_first + min((r + 1) * tpt, n));
   }
 
-  // Length on the line of one tile of a unit of `tokens` tokens.
-  __device__ __forceinline__ static int tile_length(int tokens, int tpt1) {
-    return tokens > tpt1 ? 2 : 1;
+  // Lengths on the line: of one key tile of a unit of `tokens` tokens, and of
+  // the unit's start and end.
+  __device__ __forceinline__ static int tile_length(const PagedAttnArgs& a, int tokens) {
+    return tokens > a.tpt1 ? kTileDuo : kTileOne;
+  }
+  __device__ __forceinline__ static int edge_length(const PagedAttnArgs& a, int tokens) {
+    return tokens * a.group <= kFewRows ? kEdgeFew : kEdgeRows;
+  }
+  __device__ __forceinline__ static int unit_length(const PagedAttnArgs& a, int tokens, int keys) {
+    return edge_length(a, tokens) + tiles_of(keys) * tile_length(a, tokens);
   }
 
   // Length on the line of sequence s, one kv head.
@@ -168,7 +180,7 @@ struct PagedWalk {
     const int tpt = 2 * a.tpt1;
     long long len = 0;
     for (int r = 0; r * tpt < q.n; ++r)
-      len += tiles_of(tile_keys(q.kv - q.n, q.n, tpt, r)) * tile_length(q.n - r * tpt, a.tpt1);
+      len += unit_length(a, min(tpt, q.n - r * tpt), tile_keys(q.kv - q.n, q.n, tpt, r));
     duo = q.n > a.tpt1;
     return len;
   }
@@ -196,7 +208,7 @@ struct PagedWalk {
       ntok = n > 0 ? 1 : 0;
       pos0 = pos_first;
       keys = 0;
-      flat = a.wu;
+      flat = a.unit_length;
       if (n > 0 && pos0 >= 0) {
         const long long at = static_cast<long long>(s) * a.Hkv + g;
         int cnt = a.counts[at];
@@ -215,7 +227,8 @@ struct PagedWalk {
         }
       }
       nt = tiles_of(keys);
-      w = 1;
+      w = kTileOne;
+      edge = edge_length(a, 1);
     } else {
       const int tpt = 2 * a.tpt1;
       tok0 = q0 + r * tpt;
@@ -223,8 +236,9 @@ struct PagedWalk {
       pos0 = pos_first + r * tpt;
       keys = tile_keys(pos_first, n, tpt, r);
       nt = tiles_of(keys);
-      w = tile_length(ntok, a.tpt1);
-      flat = nt * w;
+      w = tile_length(a, ntok);
+      edge = edge_length(a, ntok);
+      flat = edge + nt * w;
     }
   }
 
@@ -232,10 +246,10 @@ struct PagedWalk {
   // where that starts (not LIST).
   __device__ __forceinline__ void start(int s0, long long base0) {
     if (LIST) {
-      const long long u = x0 / a.wu;
+      const long long u = x0 / a.unit_length;
       s = static_cast<int>(u / a.Hkv);
       g = static_cast<int>(u - static_cast<long long>(s) * a.Hkv);
-      base = u * a.wu;
+      base = u * a.unit_length;
       r = 0;
       load_seq();
     } else {
@@ -248,8 +262,8 @@ struct PagedWalk {
       base += g * per_head;
       r = 0;
       while (true) {
-        const int len = tiles_of(tile_keys(pos_first, n, 2 * a.tpt1, r)) *
-                        tile_length(n - 2 * r * a.tpt1, a.tpt1);
+        const int len = unit_length(a, min(2 * a.tpt1, n - 2 * r * a.tpt1),
+                                    tile_keys(pos_first, n, 2 * a.tpt1, r));
         if (x0 < base + len || r + 1 >= nr) break;
         base += len;
         ++r;
@@ -282,8 +296,9 @@ struct PagedWalk {
   // The CTA's tiles [b, e) of the current unit: those that begin on its piece;
   // false: none of them exist.
   __device__ __forceinline__ bool range(int& b, int& e) const {
-    b = static_cast<int>((max(x0 - base, 0LL) + w - 1) / w);
-    e = static_cast<int>(min((x1 - base + w - 1) / w, static_cast<long long>(nt)));
+    const long long t0 = base + edge;
+    b = static_cast<int>((max(x0 - t0, 0LL) + w - 1) / w);
+    e = static_cast<int>(min((max(x1 - t0, 0LL) + w - 1) / w, static_cast<long long>(nt)));
     return b < e && ntok > 0;
   }
 };
@@ -601,11 +616,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
   bool any_duo = false;
   auto pieces = [&](long long total) {
     return static_cast<int>(
-        min(static_cast<long long>(gridDim.x), max(total / (any_duo ? 2 : 1), 1LL)));
+        min(static_cast<long long>(gridDim.x), max(total / (any_duo ? kTileDuo : kTileOne), 1LL)));
   };
   Found f{0, 0, 0, 0};
   if (LIST) {
-    f.total = static_cast<long long>(a.q.T) * a.Hkv * a.wu;
+    f.total = static_cast<long long>(a.q.T) * a.Hkv * a.unit_length;
   } else {
     bool duo = false;
     f = block_find(
@@ -659,15 +674,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
             qlast[buf] = -1;
             continue;
           }
-          const int q = duo ? buf : 0;
-          const int tok = sg.tok0 + q * a.tpt1;
-          const int n = min(a.tpt1, sg.ntok - q * a.tpt1);
-          if (lane == 0) mbar_arrive_expect_tx(bars.qfull(buf), n * a.group * 256u);
-          __syncwarp();
-          for (int k = lane; k < n; k += 32) {
-            const uint32_t at = s_q(buf) + k * a.group * 128u;
-            tma_load_3d(at, &tm_q, bars.qfull(buf), 0, sg.g * a.group, tok + k);
-            tma_load_3d(at + kHalfBytes, &tm_q, bars.qfull(buf), 64, sg.g * a.group, tok + k);
+          // one box of whole tokens per 64 columns; the rows behind the unit's last
+          // token are other tokens' or zero, and their results are not stored
+          if (lane == 0) {
+            const int tok = sg.tok0 + (duo ? buf * a.tpt1 : 0);
+            mbar_arrive_expect_tx(bars.qfull(buf), a.tpt1 * a.group * 256u);
+            tma_load_3d(s_q(buf), &tm_q, bars.qfull(buf), 0, sg.g * a.group, tok);
+            tma_load_3d(s_q(buf) + kHalfBytes, &tm_q, bars.qfull(buf), 64, sg.g * a.group, tok);
           }
           qlast[buf] = par;
         }
@@ -883,13 +896,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           int tb, te;
           if (!walk.range(tb, te)) continue;
           if (tb == 0 && te < walk.nt) {            // other CTAs go on with it
-            mine.c1 = piece_of(walk.base + static_cast<long long>(walk.w) * (walk.nt - 1), f.total, G);
+            mine.c1 = piece_of(walk.base + walk.edge + static_cast<long long>(walk.w) * (walk.nt - 1),
+                               f.total, G);
             mine.g = walk.g;
             mine.tok0 = walk.tok0;
             mine.ntok = walk.ntok;
           }
           int flags = (tb == 0 ? kSegStart : 0) | (tb == 0 && te == walk.nt ? kSegWhole : 0);
-          if (walk.w == 2) flags |= kSegDuo;
+          if (walk.w == kTileDuo) flags |= kSegDuo;
           if (walk.ntok * a.group <= kFewRows) flags |= kSegFew;
           if (walk.keys > 0) {
             const bool both = (flags & (kSegDuo | kSegFew)) != 0;

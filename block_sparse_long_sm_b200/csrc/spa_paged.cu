@@ -357,7 +357,8 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
   a.lists = lists;
   a.counts = counts;
   a.width = p->sink_pages + p->local_pages + p->top_pages;
-  a.wu = (int)(((long long)a.width * p->page_size + 127) / 128);
+  a.unit_length = (group <= kFewRows ? kEdgeFew : kEdgeRows) +
+                  kTileOne * (int)(((long long)a.width * p->page_size + 127) / 128);
   a.Hq = p->heads_q;
   a.Hkv = p->heads_kv;
   a.group = group;
@@ -374,7 +375,8 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
   const uint64_t cache_rows =
       (uint64_t)a.pitch * (p->num_pages - 1) + (uint64_t)p->heads_kv * p->page_size;
   CUtensorMap tq, tk, tv;
-  if (!map_rows(&tq, q->data, p->heads_q, p->tokens, q->stride_head, q->stride_token, group) ||
+  if (!map_rows(&tq, q->data, p->heads_q, p->tokens, q->stride_head, q->stride_token, group,
+                a.tpt1) ||
       !map_2d(&tk, kBF16, 2, k_cache, 128, cache_rows, 64, p->page_size, kSW128) ||
       !map_2d(&tv, kBF16, 2, v_cache, 128, cache_rows, 64, p->page_size, kSW128))
     return SPA_ERR_CUDA;
