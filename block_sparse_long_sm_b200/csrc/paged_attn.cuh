@@ -117,6 +117,7 @@ struct PagedAttnArgs {
   const int32_t* counts;     // [T][Hkv]
   int width;                 // list entries per (token, kv head)
   int unit_length;           // length on the line of a full list
+  int whole_units;           // lists: CTAs take whole units in turn
   int Hq, Hkv, group;
   int tpt1;                  // tokens per 128-row tile
   int pitch;                 // 128-element rows between pages
@@ -274,7 +275,24 @@ struct PagedWalk {
 
   __device__ __forceinline__ bool more() const { return base < x1; }
 
+  // Lists, whole units in turn: unit u is kv head u / T, token u % T, so that
+  // the CTAs are on the same head at the same time and tokens of one sequence
+  // find the pages they share in L2.
+  __device__ __forceinline__ void turn(long long u) {
+    base = u;
+    if (base >= x1) return;
+    g = static_cast<int>(u / a.q.T);
+    s = static_cast<int>(u - static_cast<long long>(g) * a.q.T);
+    r = 0;
+    load_seq();
+    set_unit();
+  }
+
   __device__ __forceinline__ void next() {
+    if (LIST && a.whole_units) {
+      turn(base + gridDim.x);
+      return;
+    }
     base += flat;
     if (base >= x1) return;
     if (++r >= nr || LIST) {
@@ -296,6 +314,11 @@ struct PagedWalk {
   // The CTA's tiles [b, e) of the current unit: those that begin on its piece;
   // false: none of them exist.
   __device__ __forceinline__ bool range(int& b, int& e) const {
+    if (LIST && a.whole_units) {
+      b = 0;
+      e = nt;
+      return ntok > 0;
+    }
     const long long t0 = base + edge;
     b = static_cast<int>((max(x0 - t0, 0LL) + w - 1) / w);
     e = static_cast<int>(min((max(x1 - t0, 0LL) + w - 1) / w, static_cast<long long>(nt)));
@@ -609,6 +632,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what the stream did before is visible
   // this CTA's piece of the line
   const int c = blockIdx.x;
   // pieces: none without a tile of a unit that spans it, so that every CTA
@@ -875,6 +899,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       PagedWalk<LIST> walk(a);
       walk.x0 = f.total * c / G;
       walk.x1 = f.total * (c + 1) / G;
+      if (LIST && a.whole_units) {
+        walk.x0 = c;
+        walk.x1 = static_cast<long long>(a.q.T) * a.Hkv;
+      }
       PagedRecord mine{-1, 0, 0, 0};
       int qn = 0, qu[2] = {0, 0};                   // next Q buffer, uses of each
       int i = 0;
@@ -892,7 +920,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         ++i;
       };
       if (c < G && walk.x0 < walk.x1 && f.s >= 0) {
-        for (walk.start(f.s, f.base); ok && walk.more(); walk.next()) {
+        if (LIST && a.whole_units)
+          walk.turn(walk.x0);
+        else
+          walk.start(f.s, f.base);
+        for (; ok && walk.more(); walk.next()) {
           int tb, te;
           if (!walk.range(tb, te)) continue;
           if (tb == 0 && te < walk.nt) {            // other CTAs go on with it
@@ -1209,76 +1241,74 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 // Joins the pieces of every unit that several CTAs share: blocks x look at the
 // record of CTA x.  O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.  A warp
-// has four rows by 32 columns: its lanes read the pieces' (m, l) side by side
-// and leave the weights in shared memory, then each lane sums four columns of
-// a row over the pieces, all loads independent (a serial merge took 17 us for
-// 8 pieces of one token).
+// has four rows by 32 columns, a lane four columns of a row; the (m, l, O) of
+// eight pieces are read side by side (a serial merge took 17 us for 8 pieces of
+// one token).
 constexpr int kCombineThreads = 256;
-constexpr int kPagedMaxCtas = 160;
+constexpr int kCombinePieces = 8;
 
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedAttnArgs a) {
-  __shared__ float weights[kCombineThreads / 32][4][kPagedMaxCtas];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedRecord rec = a.rec[blockIdx.x];
   if (rec.c1 < 0) return;
-  const int c0 = blockIdx.x, np = min(rec.c1 - c0 + 1, kPagedMaxCtas);
+  const int c0 = blockIdx.x, np = rec.c1 - c0 + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = rec.ntok * a.group;
   const int items = (rows + 3) / 4 * 4;            // row quads x four column blocks
-  // slot of piece i: the first CTA's is its second
-  auto slot = [&](int i) {
-    return a.part + (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * kPagedSlotFloats;
-  };
   for (int it = blockIdx.y * (kCombineThreads / 32) + warp; it < items;
        it += gridDim.y * (kCombineThreads / 32)) {
-    const int r = lane & 3, cg = lane >> 2;
-    const int i = min((it >> 2) * 4 + r, rows - 1);
-    const bool on = (it >> 2) * 4 + r < rows;
+    const int i = (it >> 2) * 4 + (lane & 3);
+    if (i >= rows) continue;
+    const int c4 = 8 * (it & 3) + (lane >> 2);
     const int ti = i / a.group, hh = i - ti * a.group;
     const int tile = ti >= a.tpt1 ? 1 : 0;
     const int prow = tile * 128 + (ti - tile * a.tpt1) * a.group + hh;
-    float m = -INFINITY;
-    __syncwarp();
-    for (int p = cg; p < np; p += 8) {
-      const float x = slot(p)[128 * kPagedSlotRows + prow];
-      weights[warp][r][p] = x;
-      m = fmaxf(m, x);
-    }
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f;
-    for (int p = cg; p < np; p += 8) {
-      const float x = weights[warp][r][p];
-      const float w = x == -INFINITY ? 0.f : exp2f(x - m);
-      weights[warp][r][p] = w;
-      l = fmaf(slot(p)[129 * kPagedSlotRows + prow], w, l);
-    }
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    __syncwarp();
-    const int c4 = 8 * (it & 3) + cg;
+    float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int p = 0; p < np; ++p) {
-      const float w = weights[warp][r][p];
-      const float4 x =
-          *reinterpret_cast<const float4*>(slot(p) + (c4 * kPagedSlotRows + prow) * 4);
-      acc.x = fmaf(x.x, w, acc.x);
-      acc.y = fmaf(x.y, w, acc.y);
-      acc.z = fmaf(x.z, w, acc.z);
-      acc.w = fmaf(x.w, w, acc.w);
+    for (int p0 = 0; p0 < np; p0 += kCombinePieces) {
+      float mp[kCombinePieces], lp[kCombinePieces];
+      float4 x[kCombinePieces];
+      float mn = m;
+#pragma unroll
+      for (int p = 0; p < kCombinePieces; ++p) {
+        // slot of a piece: the first CTA's is its second
+        const float* slot =
+            a.part + (2LL * (c0 + p0 + p) + (p0 + p == 0 ? 1 : 0)) * kPagedSlotFloats;
+        const bool on = p0 + p < np;
+        mp[p] = on ? slot[128 * kPagedSlotRows + prow] : -INFINITY;
+        lp[p] = on ? slot[129 * kPagedSlotRows + prow] : 0.f;
+        x[p] = on ? *reinterpret_cast<const float4*>(slot + (c4 * kPagedSlotRows + prow) * 4)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int p = 0; p < kCombinePieces; ++p) mn = fmaxf(mn, mp[p]);
+      if (mn == -INFINITY) continue;
+      const float fo = exp2f(m - mn);
+      l *= fo;
+      acc.x *= fo;
+      acc.y *= fo;
+      acc.z *= fo;
+      acc.w *= fo;
+#pragma unroll
+      for (int p = 0; p < kCombinePieces; ++p) {
+        const float w = exp2f(mp[p] - mn);
+        l = fmaf(lp[p], w, l);
+        acc.x = fmaf(x[p].x, w, acc.x);
+        acc.y = fmaf(x[p].y, w, acc.y);
+        acc.z = fmaf(x[p].z, w, acc.z);
+        acc.w = fmaf(x[p].w, w, acc.w);
+      }
+      m = mn;
     }
-    if (on) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const long long tok = static_cast<long long>(rec.tok0) + ti;
-      const int head = rec.g * a.group + hh;
-      uint2 y;
-      y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-      y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2*>(a.o.at(0, tok, head) + 4 * c4) = y;
-      if (a.lse && c4 == 0)
-        a.lse[tok * a.Hq + head] = l > 0.f ? m * 0.69314718055994531f + logf(l) : -INFINITY;
-    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const long long tok = static_cast<long long>(rec.tok0) + ti;
+    const int head = rec.g * a.group + hh;
+    uint2 y;
+    y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(a.o.at(0, tok, head) + 4 * c4) = y;
+    if (a.lse && c4 == 0)
+      a.lse[tok * a.Hq + head] = l > 0.f ? m * 0.69314718055994531f + logf(l) : -INFINITY;
   }
 }
 

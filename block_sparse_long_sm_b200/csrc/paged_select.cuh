@@ -62,7 +62,8 @@ constexpr int kScoreThreads = 128;
 constexpr int kWarpPages = 32;           // pages per warp
 constexpr int kScorePages = kWarpPages * kScoreThreads / 32;
 constexpr int kTopThreads = 256;
-constexpr int kTopKeys = 8192;           // scores kept in shared memory
+constexpr int kTopKeys = 16384;          // scores kept in shared memory
+constexpr int kTopBand = 256;            // pages ranked exactly there
 
 // Visible pages of a token and the candidates [sink, sink + n) among them.
 struct Candidates {
@@ -89,18 +90,9 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // page_top waits by itself
-  // scores of one n8 group: [row][page], [row][page] of the magnitudes
-  __shared__ float tile[kScoreThreads / 32][2][16][9];
-  const long long tg = blockIdx.x / a.chunks;
-  const int chunk = static_cast<int>(blockIdx.x - tg * a.chunks);
-  const int t0 = static_cast<int>(tg / a.Hkv);
-  const int g = static_cast<int>(tg - static_cast<long long>(t0) * a.Hkv);
-  int s;
-  const Seq q = seq_of_token(a.q, t0, s);
-  if (q.n == 0 || (t0 - q.q0) % a.tm != 0) return;        // another token's block has it
-  const int ntok = min(a.tm, q.q0 + q.n - t0);
+// Tokens t0 .. t0 + ntok - 1 of sequence s, one kv head, 32 pages of one warp.
+__device__ __forceinline__ void score_pages(const SelectArgs& a, const Seq& q, int s, int t0,
+                                            int ntok, int g, int chunk, float (*tile)[16][9]) {
   const int pos0 = q.kv - q.n + (t0 - q.q0);
   const Candidates cd = candidates(a, pos0 + ntok - 1);   // the last token sees most
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -186,22 +178,42 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectA
     __syncwarp();
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      tile[warp][0][r0 + 8 * (e >> 1)][2 * part + (e & 1)] = best[n8][e];
-      tile[warp][1][r0 + 8 * (e >> 1)][2 * part + (e & 1)] = mag[n8][e];
+      tile[0][r0 + 8 * (e >> 1)][2 * part + (e & 1)] = best[n8][e];
+      tile[1][r0 + 8 * (e >> 1)][2 * part + (e & 1)] = mag[n8][e];
     }
     __syncwarp();
     for (int i = lane; i < 8 * ntok; i += 32) {
       const int ti = i >> 3, page = i & 7;
       float x = -INFINITY, y = -INFINITY;
       for (int h = 0; h < hrows; ++h) {
-        x = fmaxf(x, tile[warp][0][ti * hrows + h][page]);
-        y = fmaxf(y, tile[warp][1][ti * hrows + h][page]);
+        x = fmaxf(x, tile[0][ti * hrows + h][page]);
+        y = fmaxf(y, tile[1][ti * hrows + h][page]);
       }
       const int c = c0 + 8 * n8 + page;
       if (c < cd.n)
         a.score[(static_cast<long long>(t0 + ti) * a.Hkv + g) * a.q.per_seq + c] =
             make_float2(x, y);
     }
+  }
+}
+
+// Block: tm token rows, one kv head, kScorePages candidates.  Rows of several
+// sequences are taken one sequence after the other.
+__global__ void __launch_bounds__(kScoreThreads, 3) page_score_kernel(const SelectArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // page_top waits by itself
+  // scores of one n8 group: [row][page], [row][page] of the magnitudes
+  __shared__ float tile[kScoreThreads / 32][2][16][9];
+  const long long bg = blockIdx.x / a.chunks;
+  const int chunk = static_cast<int>(blockIdx.x - bg * a.chunks);
+  const int block = static_cast<int>(bg / a.Hkv);
+  const int g = static_cast<int>(bg - static_cast<long long>(block) * a.Hkv);
+  const int end = min(a.q.T, (block + 1) * a.tm);
+  for (int t = block * a.tm; t < end;) {
+    int s;
+    const Seq q = seq_of_token(a.q, t, s);
+    const int next = q.n > 0 ? min(end, q.q0 + q.n) : t + 1;
+    if (q.n > 0) score_pages(a, q, s, t, next - t, g, chunk, tile[threadIdx.x >> 5]);
+    t = next;
   }
 }
 
@@ -216,6 +228,7 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 
 struct TopSmem {
   uint32_t keys[kTopKeys];
+  uint32_t band[kTopBand], exact[kTopBand], band_n;
   uint32_t hist[256];
   uint32_t red[3][kTopThreads / 32];
   uint32_t found[2];
@@ -296,9 +309,38 @@ __device__ __forceinline__ uint32_t radix_rank(int n, Key key, Use use, uint32_t
   return prefix + lo;
 }
 
+// Score of candidate i in 64 bits, rounded once: by a warp.
+__device__ __forceinline__ float exact_score(const SelectArgs& a, int s, int t, int g, int i) {
+  const int lane = threadIdx.x & 31;
+  int phys = phys_page(a.q, s, a.sink + i);
+  if (phys < 0) phys = 0;
+  const uint2* pg = reinterpret_cast<const uint2*>(
+      a.summary + (static_cast<long long>(phys) * a.Hkv + g) * 256);
+  const uint2 l2 = pg[lane], h2 = pg[32 + lane];
+  const float lo[4] = {__uint_as_float(l2.x << 16), __uint_as_float(l2.x & 0xffff0000u),
+                       __uint_as_float(l2.y << 16), __uint_as_float(l2.y & 0xffff0000u)};
+  const float hi[4] = {__uint_as_float(h2.x << 16), __uint_as_float(h2.x & 0xffff0000u),
+                       __uint_as_float(h2.y << 16), __uint_as_float(h2.y & 0xffff0000u)};
+  double best = -INFINITY;
+#pragma unroll 2
+  for (int h = 0; h < a.group; ++h) {
+    const uint2 q2 = reinterpret_cast<const uint2*>(a.xq.at(0, t, g * a.group + h))[lane];
+    const float qd[4] = {__uint_as_float(q2.x << 16), __uint_as_float(q2.x & 0xffff0000u),
+                         __uint_as_float(q2.y << 16), __uint_as_float(q2.y & 0xffff0000u)};
+    double sum = 0.0;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      sum += static_cast<double>(qd[d]) * static_cast<double>(qd[d] >= 0.f ? hi[d] : lo[d]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    best = fmax(best, sum);
+  }
+  return static_cast<float>(best);
+}
+
 __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs a) {
-  __shared__ TopSmem sm;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  extern __shared__ __align__(16) uint8_t top_smem[];
+  TopSmem& sm = *reinterpret_cast<TopSmem*>(top_smem);
   const long long tg = blockIdx.x;
   const int t = static_cast<int>(tg / a.Hkv);
   const int g = static_cast<int>(tg - static_cast<long long>(t) * a.Hkv);
@@ -325,6 +367,8 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
       out[i] = i;
   }
   if (cd.n <= a.top || a.top == 0) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the scores
+  if (tid == 0) sm.band_n = 0;
   float2* score = a.score + tg * a.q.per_seq;
   float big = 0.f;
   for (int i = tid; i < cd.n; i += kTopThreads) {
@@ -362,8 +406,32 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   const uint32_t need = a.top - in;                 // of those between; at least one
   // the smallest key kept, and how many of the pages that have it
   uint32_t least = bottom, equal = 0xffffffffu;
-  if (between > need) {
-    // exact scores of the pages between, a warp each
+  bool exact = between > need;
+  if (exact && cd.n <= kTopKeys && between <= kTopBand) {
+    // the pages between, ranked exactly in shared memory: the kept ones get the
+    // largest key, the others the smallest
+    for (int i = tid; i < cd.n; i += kTopThreads) {
+      const uint32_t u = sm.keys[i];
+      if (u <= top && u >= bottom) sm.band[atomicAdd(&sm.band_n, 1u)] = i;
+    }
+    __syncthreads();
+    for (uint32_t k = warp; k < between; k += kTopThreads / 32) {
+      const float x = exact_score(a, s, t, g, static_cast<int>(sm.band[k]));
+      if (lane == 0) sm.exact[k] = ordered(x);
+    }
+    __syncthreads();
+    if (static_cast<uint32_t>(tid) < between) {
+      const uint32_t me = sm.exact[tid], at = sm.band[tid];
+      uint32_t better = 0;
+      for (uint32_t k = 0; k < between; ++k)
+        better += sm.exact[k] > me || (sm.exact[k] == me && sm.band[k] < at);
+      sm.keys[at] = better < need ? 0xffffffffu : 0u;
+    }
+    __syncthreads();
+    exact = false;
+  } else if (exact) {
+    // many of them (equal pages), or more candidates than fit: in the score
+    // array, marked by a negative magnitude
     __syncthreads();
     for (int base = warp * 32; base < cd.n; base += kTopThreads) {
       const uint32_t u = base + lane < cd.n ? key(base + lane) : 0u;
@@ -371,30 +439,8 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
       while (todo) {
         const int i = base + __ffs(todo) - 1;
         todo &= todo - 1;
-        int phys = phys_page(a.q, s, a.sink + i);
-        if (phys < 0) phys = 0;
-        const __nv_bfloat16* pg = a.summary + (static_cast<long long>(phys) * a.Hkv + g) * 256;
-        float lo[4], hi[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          lo[d] = __bfloat162float(pg[4 * lane + d]);
-          hi[d] = __bfloat162float(pg[128 + 4 * lane + d]);
-        }
-        double best = -INFINITY;
-        for (int h = 0; h < a.group; ++h) {
-          const __nv_bfloat16* x = a.xq.at(0, t, g * a.group + h);
-          double sum = 0.0;
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const float qd = __bfloat162float(x[4 * lane + d]);
-            sum += static_cast<double>(qd) * static_cast<double>(qd >= 0.f ? hi[d] : lo[d]);
-          }
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          best = fmax(best, sum);
-        }
-        // marked by a negative magnitude
-        if (lane == 0) score[i] = make_float2(static_cast<float>(best), -1.0f);
+        const float x = exact_score(a, s, t, g, i);
+        if (lane == 0) score[i] = make_float2(x, -1.0f);
       }
     }
     __syncthreads();
@@ -406,7 +452,6 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   }
   // pages above the border, and of those between the ones above `least` with
   // the first `equal` that have it
-  const bool exact = between > need;
   const int per = (cd.n + kTopThreads - 1) / kTopThreads;
   const int i0 = min(cd.n, tid * per), i1 = min(cd.n, i0 + per);
   // 0 dropped, 1 kept, 2 equal to the least

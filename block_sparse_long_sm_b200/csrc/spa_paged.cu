@@ -20,7 +20,6 @@ using namespace spa;
 
 // CTAs of the attention: one per SM of the chip's 148.
 constexpr int kPagedGrid = 148;
-static_assert(kPagedGrid <= kPagedMaxCtas, "weights of the combine");
 
 bool rows_ok(const spa_rows* r) {
   return r && r->data && aligned16(r->data) && r->stride_batch % 8 == 0 &&
@@ -161,27 +160,32 @@ spa_status paged_checks(const spa_paged_params* p, const spa_rows* q, const int3
 
 // Launch that may begin before the stream's previous kernel has ended; the
 // kernel itself waits for that one's results.
-template <typename K, typename A>
-bool launch_after(K kernel, dim3 grid, unsigned threads, cudaStream_t stream, const A& args) {
+template <typename... P, typename... A>
+bool launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+                  cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
 template <bool LIST>
 bool launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                   const PagedAttnArgs& a, int combine_y, cudaStream_t stream) {
   if (set_smem(paged_attn_kernel<LIST>, kPagedSmemBytes) != cudaSuccess) return false;
-  paged_attn_kernel<LIST><<<kPagedGrid, kPagedThreads, kPagedSmemBytes, stream>>>(tq, tk, tv, a);
-  if (cudaGetLastError() != cudaSuccess) return false;
-  return launch_after(paged_combine_kernel, dim3(kPagedGrid, combine_y), kCombineThreads, stream, a);
+  if (!launch_after(paged_attn_kernel<LIST>, dim3(kPagedGrid), kPagedThreads, kPagedSmemBytes,
+                    stream, tq, tk, tv, a))
+    return false;
+  if (a.whole_units) return true;
+  return launch_after(paged_combine_kernel, dim3(kPagedGrid, combine_y), kCombineThreads, 0,
+                      stream, a);
 }
 
 }  // namespace
@@ -314,17 +318,26 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
   a.local = p->local_pages;
   a.top = p->top_pages;
   a.width = a.sink + a.local + a.top;
-  a.tm = a.group <= 16 ? 16 / a.group : 1;
+  // tokens beside one another share a block's loads when they can be of one sequence
+  a.tm = a.group <= 16 && p->tokens > p->seqs ? 16 / a.group : 1;
   const long long most = (long long)p->pages_per_seq - a.sink - a.local;   // candidates
   const long long tg = (long long)p->tokens * p->heads_kv;
+  if (tg > INT_MAX) return SPA_ERR_UNSUPPORTED;
+  if (set_smem(page_top_kernel, sizeof(TopSmem)) != cudaSuccess) return SPA_ERR_CUDA;
   if (most > a.top && a.top > 0) {
     a.chunks = (int)((most + kScorePages - 1) / kScorePages);
-    if (tg * a.chunks > INT_MAX) return SPA_ERR_UNSUPPORTED;
-    page_score_kernel<<<(unsigned)(tg * a.chunks), kScoreThreads, 0, stream>>>(a);
+    const long long blocks = ((long long)p->tokens + a.tm - 1) / a.tm * p->heads_kv * a.chunks;
+    if (blocks > INT_MAX) return SPA_ERR_UNSUPPORTED;
+    page_score_kernel<<<(unsigned)blocks, kScoreThreads, 0, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPA_ERR_CUDA;
+    // (begins while the scores are computed: it reads the lengths meanwhile)
+    return launch_after(page_top_kernel, dim3((unsigned)tg), kTopThreads, sizeof(TopSmem), stream,
+                        a)
+               ? SPA_OK
+               : SPA_ERR_CUDA;
   }
-  return launch_after(page_top_kernel, dim3((unsigned)tg), kTopThreads, stream, a) ? SPA_OK
-                                                                                   : SPA_ERR_CUDA;
+  page_top_kernel<<<(unsigned)tg, kTopThreads, sizeof(TopSmem), stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SPA_OK : SPA_ERR_CUDA;
 }
 
 SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* q,
@@ -359,6 +372,9 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
   a.width = p->sink_pages + p->local_pages + p->top_pages;
   a.unit_length = (group <= kFewRows ? kEdgeFew : kEdgeRows) +
                   kTileOne * (int)(((long long)a.width * p->page_size + 127) / 128);
+  // Eight or more units per CTA: whole ones in turn (the last round costs at
+  // most an eighth, and nothing is left to join).
+  a.whole_units = lists && (long long)p->tokens * p->heads_kv >= 8LL * kPagedGrid;
   a.Hq = p->heads_q;
   a.Hkv = p->heads_kv;
   a.group = group;

@@ -104,3 +104,34 @@ def test_no_candidates_anywhere():
         _, sm, lists, counts, _ = run_select(b, sink, local, top)
         check_lists(b, lists, counts, expected(b, sm, sink, local, top))
     b.ok()
+
+
+@pytest.mark.parametrize("top", [1, 700, 16000])
+def test_more_candidates_than_fit_in_shared_memory(top):
+    # 17000 pages of one sequence that share a few physical pages: many equal scores as well
+    b = Batch(2, 1, 16, [(1, 16 * 20)], seed=6)
+    n = 17000
+    rng = np.random.default_rng(1)
+    b.table = rng.integers(0, 20, size=(1, n)).astype(np.int32)
+    b.per_seq = n
+    b.table_gpu = torch.from_numpy(b.table).cuda()
+    b.kv = [n * 16]
+    b.kv_gpu = torch.tensor(b.kv, dtype=torch.int32).cuda()
+    sm = bits_of(rng.standard_normal((b.num_pages, 1, 2, D)))
+    sm[:, :, 1] = bits_of(np.maximum(f64(sm[:, :, 0]), f64(sm[:, :, 1])))
+    _, _, lists, counts, _ = run_select(b, 1, 1, top, summary=sm)
+    u = op.page_bounds(f64(b.qkv[0, :2]), f64(sm[:, 0, 0]), f64(sm[:, 0, 1]))
+    want = op.select_pages(n * 16 - 1, 16, 1, 1, top, lambda a, z: u[b.table[0, a:z]])
+    check_lists(b, lists, counts, {(0, 0): want})
+    b.ok()
+
+
+def test_many_tokens_take_whole_units_in_turn():
+    b = Batch(4, 2, 16, [(500, 900), (3, 700), (120, 130)], seed=7, pad_rows=5)
+    p, sm, lists, counts, ws = run_select(b, 1, 2, 9)
+    pick = set(int(t) for t in np.random.default_rng(0).permutation(623)[:50]) | {0, 499, 500, 503, 622}
+    want = expected(b, sm, 1, 2, 9)
+    check_lists(b, lists, counts, want)
+    o, lse = attend(b, p, lists, counts, ws=ws)
+    check_attention(b, o, lse, pages_of=lambda t, g: want[(t, g)], rows=pick)
+    b.ok()
