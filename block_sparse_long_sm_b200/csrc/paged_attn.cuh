@@ -86,9 +86,13 @@ struct PagedSeg {
   int g;         // kv head
   int seq;       // block table row
   int pad[3];
+  int page[32];  // physical numbers of the first 32 pages from tile tb on (-1: none)
 };
-static_assert(sizeof(PagedSeg) == 48, "ring entries");
+static_assert(sizeof(PagedSeg) == 176, "ring entries");
 constexpr int kPagedSegs = 4;
+struct FewSeg {   // what its eight warps need of a segment of few rows
+  int tb, te, flags, keys, tok0, ntok, pos0, g;
+};
 constexpr int kSegDuo = 1;      // two row tiles
 constexpr int kSegStart = 2;    // holds the unit's first tile
 constexpr int kSegWhole = 4;    // holds all of them
@@ -147,11 +151,11 @@ struct PagedWalk {
   const PagedAttnArgs& a;
   long long x0, x1;          // the CTA's piece of the line
   long long base;            // where the current unit starts on it
-  int s, g, r;               // sequence (LIST: token row), kv head, row tile
+  int s = 0, g = 0, r = 0;   // sequence (LIST: token row), kv head, row tile
   int q0, n, pos_first;      // of the sequence
   int nr;                    // its row tiles
   // the current unit
-  int seq, tok0, ntok, pos0, keys, nt;
+  int seq = 0, tok0 = 0, ntok = 0, pos0 = 0, keys = 0, nt = 0;
   int w, edge, flat;         // lengths on the line: a tile, what precedes them, all
 
   __device__ __forceinline__ explicit PagedWalk(const PagedAttnArgs& args) : a(args) {}
@@ -326,6 +330,26 @@ struct PagedWalk {
   }
 };
 
+// Physical number of page j of a unit's keys; -1 behind its last.  A bad entry is
+// reported, and any page does for it.
+template <bool LIST>
+__device__ __forceinline__ int unit_page(const PagedAttnArgs& a, int j, int keys, int tok, int g,
+                                         int seq, int pos) {
+  if (j >= (keys + a.q.page - 1) >> a.q.shift) return -1;
+  int lp = j;
+  if (LIST) {
+    const int32_t* list = a.lists + (static_cast<long long>(tok) * a.Hkv + g) * a.width;
+    lp = list[j];
+    const int before = j > 0 ? list[j - 1] : -1;
+    if (lp <= before || lp < 0 || lp > (pos >> a.q.shift)) {
+      atomicOr(a.q.err, kErrBadIndex);
+      lp = 0;
+    }
+  }
+  const int p = phys_page(a.q, seq, lp);
+  return p < 0 ? 0 : p;
+}
+
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
@@ -372,14 +396,16 @@ struct PagedBars {
 };
 static_assert(kPagedKStages == 3 && kPagedVStages == 2, "barrier numbers");
 // Offsets behind the barriers (36 of them).
-constexpr int kPagedTmem = 304, kPagedSegRing = 320, kPagedFind = 512, kPagedMl = 1024;
+// The search of a CTA's piece is over before the ring is used.
+constexpr int kPagedTmem = 304, kPagedSegRing = 320, kPagedFind = 320, kPagedMl = 1024;
+static_assert(kPagedSegRing + kPagedSegs * sizeof(PagedSeg) <= kPagedMl, "ring");
 
 // A segment of few rows (see above), by one of the eight warps; kt: the CTA's
 // tiles before it, parity: of this segment's exchange, uses1: of accumulator 1
 // before it.  False when a wait gave up.  A function of its own, so that its
 // registers and those of the 128-row softmax are allotted apart.
 template <bool LIST>
-__device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const PagedSeg sg, uint8_t* smem,
+__device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const FewSeg sg, uint8_t* smem,
                                          uint32_t s_base, uint32_t b0, const WaitCtx wc, int kt,
                                          uint32_t parity, int uses1) {
   const PagedBars bars{b0};
@@ -668,10 +694,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
   const WaitCtx wc{abort_flag, a.q.err, a.wait_ns};
   // Segment i of the piece, copied out of the ring; false at its end.
-  auto take = [&](int i, PagedSeg& sg) -> bool {
+  auto take = [&](int i, PagedSeg& sg, int* page = nullptr) -> bool {
     const int r = i % kPagedSegs;
     if (!warp_wait(bars.wfull(r), (i / kPagedSegs) & 1, wc)) return false;
-    sg = segs[r];
+    const PagedSeg& x = segs[r];
+    sg.tb = x.tb;
+    sg.te = x.te;
+    sg.flags = x.flags;
+    sg.keys = x.keys;
+    sg.tok0 = x.tok0;
+    sg.ntok = x.ntok;
+    sg.pos0 = x.pos0;
+    sg.g = x.g;
+    sg.seq = x.seq;
+    if (page) *page = x.page[lane];
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.wempty(r));
     return sg.te >= 0;
@@ -686,7 +722,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       int kt = 0, qlast[2] = {-1, -1};              // key tiles; parity of the Q loads in flight
       bool ok = true;
       PagedSeg sg;
-      for (int i = 0; ok && take(i, sg); ++i) {
+      int mine = -1;                                // the lane's page of the first batch
+      for (int i = 0; ok && take(i, sg, &mine); ++i) {
         if (sg.keys == 0) continue;
         const bool duo = (sg.flags & kSegDuo) != 0, few = (sg.flags & kSegFew) != 0;
         for (int buf = 0; buf < 2; ++buf) {
@@ -710,30 +747,22 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         if (!ok) break;
         __syncwarp();
-        // lane l < ppt: page l of the tile; its physical number is fetched one
-        // tile ahead so that the table's latency overlaps the wait for a stage
-        const int32_t* list = nullptr;
-        int npages = (sg.keys + a.q.page - 1) >> a.q.shift;
-        if (LIST) list = a.lists + (static_cast<long long>(sg.tok0) * a.Hkv + sg.g) * a.width;
-        auto fetch = [&](int t) -> int {
-          const int j = t * ppt + lane;
-          if (lane >= ppt || j >= npages) return -1;
-          int lp = j;
-          if (LIST) {
-            lp = list[j];
-            const int before = j > 0 ? list[j - 1] : -1;
-            if (lp <= before || lp < 0 || lp > (sg.pos0 >> a.q.shift)) {
-              atomicOr(a.q.err, kErrBadIndex);
-              lp = 0;
-            }
-          }
-          const int p = phys_page(a.q, sg.seq, lp);
-          return p < 0 ? 0 : p;                     // reported; any page will do
+        // Pages come in batches of 32, one per lane: the first with the segment,
+        // each further one read while the tiles before it are loaded.
+        const int per = 32 / ppt;                   // tiles per batch
+        auto batch = [&](int k) {
+          return unit_page<LIST>(a, (sg.tb + k * per) * ppt + lane, sg.keys, sg.tok0, sg.g, sg.seq,
+                                 sg.pos0);
         };
-        int ahead = fetch(sg.tb);
+        int cur = mine, ahead = batch(1);
         for (int t = sg.tb; t < sg.te; ++t, ++kt) {
-          const int phys = ahead;
-          if (t + 1 < sg.te) ahead = fetch(t + 1);
+          const int in = (t - sg.tb) % per;         // tile of the batch
+          if (in == 0 && t > sg.tb) {
+            cur = ahead;
+            ahead = batch((t - sg.tb) / per + 1);
+          }
+          const int from = __shfl_sync(0xffffffffu, cur, (in * ppt + lane) & 31);
+          const int phys = lane < ppt ? from : -1;
           const uint32_t live = __popc(__ballot_sync(0xffffffffu, phys >= 0));
           const int row = phys * a.pitch + (sg.g << a.q.shift);
           const int ks = kt % kPagedKStages, vs = kt % kPagedVStages;
@@ -894,7 +923,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         mbar_drain(bars.drain(), 0, a.wait_ns);
       }
       __syncwarp();
-    } else if (warp == 10 && lane == 0) {
+    } else if (warp == 10) {
       // ----------------------------------------------- the CTA's segments
       PagedWalk<LIST> walk(a);
       walk.x0 = f.total * c / G;
@@ -907,16 +936,36 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       int qn = 0, qu[2] = {0, 0};                   // next Q buffer, uses of each
       int i = 0;
       bool ok = true;
-      auto hand = [&](const PagedSeg& sg) {
+      auto hand = [&](int tb, int te, int flags) {
         const int r = i % kPagedSegs;
+        const int page = te >= 0 ? unit_page<LIST>(a, tb * (128 >> a.q.shift) + lane, walk.keys,
+                                                   walk.tok0, walk.g, walk.seq, walk.pos0)
+                                 : -1;
         if (i >= kPagedSegs) {
           // a long wait as a rule: the warp sleeps in between, out of the others' way
           const uint32_t parity = (i / kPagedSegs - 1) & 1;
-          for (int k = 0; k < 64 && !mbar_try_wait(bars.wempty(r), parity); ++k) __nanosleep(500);
-          if (!(ok = mbar_wait(bars.wempty(r), parity, wc))) return;
+          bool there = false;
+          for (int k = 0; k < 64 && !there; ++k) {
+            there = __all_sync(0xffffffffu, mbar_try_wait(bars.wempty(r), parity));
+            if (!there) __nanosleep(500);
+          }
+          if (!there && !(ok = warp_wait(bars.wempty(r), parity, wc))) return;
         }
-        segs[r] = sg;
-        mbar_arrive(bars.wfull(r));
+        PagedSeg& x = segs[r];
+        x.page[lane] = page;
+        if (lane == 0) {
+          x.tb = tb;
+          x.te = te;
+          x.flags = flags;
+          x.keys = walk.keys;
+          x.tok0 = walk.tok0;
+          x.ntok = walk.ntok;
+          x.pos0 = walk.pos0;
+          x.g = walk.g;
+          x.seq = walk.seq;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.wfull(r));
         ++i;
       };
       if (c < G && walk.x0 < walk.x1 && f.s >= 0) {
@@ -947,12 +996,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
             }
             if (!both) qn ^= 1;
           }
-          hand(PagedSeg{tb, te, flags, walk.keys, walk.tok0, walk.ntok, walk.pos0, walk.g,
-                        walk.seq, {0, 0, 0}});
+          hand(tb, te, flags);
         }
       }
-      a.rec[c] = mine;
-      if (ok) hand(PagedSeg{0, -1, 0, 0, 0, 0, 0, 0, 0, {0, 0, 0}});
+      if (lane == 0) a.rec[c] = mine;
+      if (ok) hand(0, -1, 0);
     }
   } else {
     // ------------------------------------------------------------- softmax
@@ -978,7 +1026,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       const int te = sg.te, flags = sg.flags;
       if (te < 0) break;
       if ((flags & kSegFew) && sg.keys > 0) {
-        const PagedSeg own{sg.tb, te, flags, sg.keys, sg.tok0, sg.ntok, sg.pos0, sg.g, sg.seq, {0, 0, 0}};
+        const FewSeg own{sg.tb, te, flags, sg.keys, sg.tok0, sg.ntok, sg.pos0, sg.g};
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.wempty(i % kPagedSegs));
         if (!(ok = few_segment<LIST>(a, own, smem, s_base, b0, wc, kt, fc++ & 1, oc[1]))) break;

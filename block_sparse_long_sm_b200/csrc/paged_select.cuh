@@ -227,13 +227,19 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 }
 
 struct TopSmem {
-  uint32_t keys[kTopKeys];
   uint32_t band[kTopBand], exact[kTopBand], band_n;
   uint32_t hist[256];
   uint32_t red[3][kTopThreads / 32];
   uint32_t found[2];
   unsigned long long sums[kTopThreads / 32];
+  uint32_t keys[1];                      // [cap]: as many as pages_per_seq, up to kTopKeys
 };
+__host__ __device__ constexpr int top_keys(int per_seq) {
+  return per_seq < kTopKeys ? per_seq : kTopKeys;
+}
+__host__ __device__ constexpr uint32_t top_smem_bytes(int per_seq) {
+  return static_cast<uint32_t>(sizeof(TopSmem)) + 4u * top_keys(per_seq);
+}
 
 // The key of rank `rank` (from 1, largest first) among key(i), i < n, where
 // use(i): eight bits at a time below the highest bit that the keys differ in.
@@ -369,19 +375,20 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   if (cd.n <= a.top || a.top == 0) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the scores
   if (tid == 0) sm.band_n = 0;
+  const int cap = top_keys(a.q.per_seq);
   float2* score = a.score + tg * a.q.per_seq;
   float big = 0.f;
   for (int i = tid; i < cd.n; i += kTopThreads) {
     const float2 x = score[i];
     big = fmaxf(big, x.y);
-    if (i < kTopKeys) sm.keys[i] = ordered(x.x);
+    if (i < cap) sm.keys[i] = ordered(x.x);
   }
   big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
   if (lane == 0) sm.red[2][warp] = __float_as_uint(big);
   __syncthreads();
   big = __uint_as_float(
       __reduce_max_sync(0xffffffffu, sm.red[2][lane & (kTopThreads / 32 - 1)]));
-  auto key = [&](int i) { return i < kTopKeys ? sm.keys[i] : ordered(score[i].x); };
+  auto key = [&](int i) { return i < cap ? sm.keys[i] : ordered(score[i].x); };
   uint32_t rank = a.top;
   uint32_t edge = radix_rank(cd.n, key, [](int) { return true; }, rank, sm);
   // keys above `top` are kept, below `bottom` are not
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   // the smallest key kept, and how many of the pages that have it
   uint32_t least = bottom, equal = 0xffffffffu;
   bool exact = between > need;
-  if (exact && cd.n <= kTopKeys && between <= kTopBand) {
+  if (exact && cd.n <= cap && between <= kTopBand) {
     // the pages between, ranked exactly in shared memory: the kept ones get the
     // largest key, the others the smallest
     for (int i = tid; i < cd.n; i += kTopThreads) {
@@ -458,7 +465,7 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   auto verdict = [&](int i) -> int {
     uint32_t u;
     bool inside;
-    if (i < kTopKeys) {
+    if (i < cap) {
       u = sm.keys[i];
       inside = u <= top && u >= bottom;
     } else {
@@ -469,7 +476,7 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     }
     if (!inside) return u > top ? 1 : 0;
     if (!exact) return 1;
-    if (i < kTopKeys) u = ordered(score[i].x);
+    if (i < cap) u = ordered(score[i].x);
     return u > least ? 1 : u == least ? 2 : 0;
   };
   unsigned long long mine = 0;                      // kept in the high word, equal in the low

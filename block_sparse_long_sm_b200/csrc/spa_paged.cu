@@ -323,7 +323,7 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
   const long long most = (long long)p->pages_per_seq - a.sink - a.local;   // candidates
   const long long tg = (long long)p->tokens * p->heads_kv;
   if (tg > INT_MAX) return SPA_ERR_UNSUPPORTED;
-  if (set_smem(page_top_kernel, sizeof(TopSmem)) != cudaSuccess) return SPA_ERR_CUDA;
+  if (set_smem(page_top_kernel, top_smem_bytes(INT_MAX)) != cudaSuccess) return SPA_ERR_CUDA;
   if (most > a.top && a.top > 0) {
     a.chunks = (int)((most + kScorePages - 1) / kScorePages);
     const long long blocks = ((long long)p->tokens + a.tm - 1) / a.tm * p->heads_kv * a.chunks;
@@ -331,12 +331,12 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
     page_score_kernel<<<(unsigned)blocks, kScoreThreads, 0, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPA_ERR_CUDA;
     // (begins while the scores are computed: it reads the lengths meanwhile)
-    return launch_after(page_top_kernel, dim3((unsigned)tg), kTopThreads, sizeof(TopSmem), stream,
-                        a)
+    return launch_after(page_top_kernel, dim3((unsigned)tg), kTopThreads,
+                        top_smem_bytes(p->pages_per_seq), stream, a)
                ? SPA_OK
                : SPA_ERR_CUDA;
   }
-  page_top_kernel<<<(unsigned)tg, kTopThreads, sizeof(TopSmem), stream>>>(a);
+  page_top_kernel<<<(unsigned)tg, kTopThreads, top_smem_bytes(p->pages_per_seq), stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? SPA_OK : SPA_ERR_CUDA;
 }
 
