@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
       return;
     }
     const Angles ang = load_angles(a.r, pos, li);
+    const NormWeights nw = load_weights(a.qw, li);
     const int h0 = static_cast<int>(w % a.groups) * a.heads_per_warp;
     const int h1 = min(h0 + a.heads_per_warp, a.Hq);
 #pragma unroll 4
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
       Row16 x;
       unpack8(*reinterpret_cast<const uint4*>(src + 8 * li), x.x);
       unpack8(*reinterpret_cast<const uint4*>(src + 64 + 8 * li), x.x + 8);
-      norm_rotate(x, a.qw != nullptr, a.qw, a.r, ang, li);
+      norm_rotate(x, a.qw != nullptr, true, nw, a.r, ang, li);
       if (on) {
         __nv_bfloat16* dst = a.qo.at(0, t, h);
         *reinterpret_cast<uint4*>(dst + 8 * li) = pack8(x.x);
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
       mx[i] = fmaxf(mx[i], x.x[i]);
     }
   };
+  const NormWeights nw = load_weights(a.kw, li);
 #pragma unroll 2
   for (int base = lo; base < hi; base += kAppendSlots) {
     const int pos = base + slot;
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
     const uint4 v0 = *reinterpret_cast<const uint4*>(vs + 8 * li);
     const uint4 v1 = *reinterpret_cast<const uint4*>(vs + 64 + 8 * li);
     const Angles ang = load_angles(a.r, on ? pos : 0, li);
-    norm_rotate(x, a.kw != nullptr, a.kw, a.r, ang, li);
+    norm_rotate(x, a.kw != nullptr, true, nw, a.r, ang, li);
     if (on) {
       const int r = pos & (v.page - 1);
       *reinterpret_cast<uint4*>(kp + r * 128 + 8 * li) = pack8(x.x);

@@ -98,25 +98,39 @@ __device__ __forceinline__ Angles load_angles(const RopeSpec& r, int pos, int li
   return a;
 }
 
-// Norm and rotation of the row held by the eight lanes; every lane of the warp
-// takes part (shuffles), so `norm` is the same for all of them: whether any row
-// of this call has a weight.  weight: this row's, or null.
-__device__ __forceinline__ void norm_rotate(Row16& v, bool norm, const __nv_bfloat16* weight,
+// The lane's sixteen weights of a row's norm, as they come (1 without).
+struct NormWeights {
+  uint4 lo, hi;
+};
+__device__ __forceinline__ NormWeights load_weights(const __nv_bfloat16* weight, int li) {
+  NormWeights n;
+  n.lo = n.hi = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+  if (weight != nullptr) {
+    n.lo = *reinterpret_cast<const uint4*>(weight + 8 * li);
+    n.hi = *reinterpret_cast<const uint4*>(weight + 64 + 8 * li);
+  }
+  return n;
+}
+
+// Norm (of this row when `mine`; `any`, the same for the whole warp: of some
+// row) and rotation of the row held by the eight lanes; every lane of the warp
+// takes part (shuffles).  rsqrtf is off by at most 2 units in the last place of fp32.
+__device__ __forceinline__ void norm_rotate(Row16& v, bool any, bool mine, const NormWeights& n,
                                             const RopeSpec& r, const Angles& a, int li) {
-  if (norm) {
+  if (any) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) ss = fmaf(v.x[i], v.x[i], ss);
 #pragma unroll
     for (int o = 1; o < kRowLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (weight != nullptr) {
-      const float f = 1.0f / sqrtf(ss * (1.0f / 128.0f) + r.eps);
-      float w[16];
-      unpack8(*reinterpret_cast<const uint4*>(weight + 8 * li), w);
-      unpack8(*reinterpret_cast<const uint4*>(weight + 64 + 8 * li), w + 8);
+    const float f = mine ? rsqrtf(ss * (1.0f / 128.0f) + r.eps) : 1.0f;
+    float w[8];
+    unpack8(n.lo, w);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v.x[i] = v.x[i] * f * w[i];
-    }
+    for (int i = 0; i < 8; ++i) v.x[i] = v.x[i] * f * w[i];
+    unpack8(n.hi, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.x[8 + i] = v.x[8 + i] * f * w[i];
   }
   if (r.rot == 0) return;
   if (r.interleaved) {
@@ -162,10 +176,14 @@ struct NormRopeArgs {
 
 constexpr int kRopeThreads = 256;
 
-// One warp: one token, heads_per_warp of its heads, four at a time.  The
-// angles are loaded once per warp.  The rows of a step are independent, so the
-// loop is unrolled to keep several 16-byte loads per lane in flight.
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeArgs a) {
+// One warp: one token, heads_per_warp of its heads, four at a time.  The angles
+// are loaded once per warp (40 heads per warp instead of 20: 259 us instead of
+// 274 on 65536 tokens of 40 heads, 5.3 TB/s), the weights with every row (from
+// L1; kept in registers, in a loop per side, they cost more in loads under way
+// than they save: 299 us).  The rows of a step are independent, so the loop is
+// unrolled to keep several 16-byte loads per lane in flight, and four blocks
+// per SM bound the registers (with as many as the compiler likes: 291 us).
+__global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const NormRopeArgs a) {
   const long long w = (static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x) >> 5;
   if (w >= a.warps) return;
   const int lane = threadIdx.x & 31, li = lane & 7, slot = lane >> 3;
@@ -191,7 +209,9 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeA
     Row16 v;
     unpack8(*reinterpret_cast<const uint4*>(src + 8 * li), v.x);
     unpack8(*reinterpret_cast<const uint4*>(src + 64 + 8 * li), v.x + 8);
-    norm_rotate(v, a.qw != nullptr || a.kw != nullptr, isq ? a.qw : a.kw, a.r, ang, li);
+    const __nv_bfloat16* weight = isq ? a.qw : a.kw;
+    norm_rotate(v, a.qw != nullptr || a.kw != nullptr, weight != nullptr,
+                load_weights(weight, li), a.r, ang, li);
     if (on) {
       __nv_bfloat16* dst = isq ? a.qo.at(b, t, hr) : a.ko.at(b, t, hr);
       *reinterpret_cast<uint4*>(dst + 8 * li) = pack8(v.x);

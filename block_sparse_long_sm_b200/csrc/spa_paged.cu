@@ -111,12 +111,12 @@ RopeSpec rope_of(const spa_rope_params* r, const float* table) {
   return s;
 }
 
-// Heads a warp takes of one token: all of a large batch's angles are loaded
-// once per 20 heads, a small one is spread over more warps instead.
+// Heads a warp takes of one token: a large batch's angles are loaded once per
+// 40 heads, a small one is spread over more warps instead.
 int heads_per_warp(long long tokens, int heads) {
   const long long quads = tokens * ((heads + 3) / 4);
   int per = 4;
-  while (per < 20 && quads * 4 / per > 148LL * 32) per += 4;
+  while (per < 40 && quads * 4 / per > 148LL * 32) per += 4;
   return per;
 }
 
