@@ -187,6 +187,8 @@ _raw_stream = getattr(getattr(_torch, "_C", None), "_cuda_getCurrentRawStream", 
 
 
 def _stream(s) -> Optional[int]:
+    if s.__class__ is int:
+        return s
     if s is None:
         try:
             if _raw_stream is not None:
@@ -194,9 +196,7 @@ def _stream(s) -> Optional[int]:
             return _torch.cuda.current_stream().cuda_stream
         except Exception:  # pragma: no cover - no torch / no device
             return None
-    if isinstance(s, int):
-        return s
-    return s.cuda_stream
+    return s if isinstance(s, int) else s.cuda_stream
 
 
 def _nbytes(x) -> int:
@@ -330,7 +330,7 @@ def _rows(x, batch, tokens, heads, name):
     if sh[-3:] != (tokens, heads, 128) or (sh[0] != batch if len(sh) == 4 else batch != 1) \
             or not 3 <= len(sh) <= 4:
         raise ValueError(f"{name}: shape {tuple(sh)}, wanted {(batch, tokens, heads, 128)}")
-    if x.dtype is not _torch.bfloat16:
+    if x.dtype is not _BF16:
         raise TypeError(f"{name}: {x.dtype}, wanted torch.bfloat16")
     if st[-1] != 1 and x.numel():
         raise ValueError(f"{name}: the 128 elements of a row have to be contiguous")
@@ -350,23 +350,15 @@ def _flat(x, dtype, count, name):
     return x.data_ptr()
 
 
-def _i32(x, count, name):
-    return _flat(x, _torch.int32, count, name) if x.__class__ is not int else x
-
-
-def _bf16(x, count, name):
-    return _flat(x, _torch.bfloat16, count, name) if x.__class__ is not int else x
-
-
-def _f32(x, count, name):
-    return _flat(x, _torch.float32, count, name) if x.__class__ is not int else x
+_I32, _BF16, _F32, _U32 = (getattr(_torch, t, None)
+                           for t in ("int32", "bfloat16", "float32", "uint32"))
 
 
 def _word(x):
     """Address of the error word: one int32 or uint32."""
     if x is None or x.__class__ is int:
         return x
-    return _flat(x, x.dtype if x.dtype is _torch.uint32 else _torch.int32, 1, "error")
+    return _flat(x, _U32 if x.dtype is _U32 else _I32, 1, "error")
 
 
 def _device(*tensors):
@@ -385,10 +377,18 @@ def _device(*tensors):
     return -1 if dev is None else dev
 
 
+_current_device = getattr(getattr(_torch, "_C", None), "_cuda_getDevice", None) or (
+    lambda: _torch.cuda.current_device())
+
+
 def _call(fn, dev, stream, *args):
     """fn(*args, stream) with the tensors' device current, on the stream given or on that
     device's current one."""
-    if dev < 0 or dev == _torch.cuda.current_device():
+    if dev < 0:
+        return fn(*args, _stream(stream))
+    if stream is None and _raw_stream is not None:
+        stream = _raw_stream(dev)
+    if dev == _current_device():
         return fn(*args, _stream(stream))
     with _torch.cuda.device(dev):
         return fn(*args, _stream(stream))
@@ -402,7 +402,7 @@ def _cache(p: SpaPagedParams, x, name):
     if x.shape != (p.num_pages, heads, page, 128):
         raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted "
                          f"{(p.num_pages, heads, page, 128)}")
-    if x.dtype is not _torch.bfloat16:
+    if x.dtype is not _BF16:
         raise TypeError(f"{name}: {x.dtype}, wanted torch.bfloat16")
     pitch = p.page_stride or heads * page * 128
     st = x.stride()
@@ -421,9 +421,9 @@ def sparse_qk_norm_rope(params: SpaRopeParams, q, k, q_weight, k_weight, positio
     dev = _device(q, k, q_weight, k_weight, positions, table, q_out, k_out, error)
     return _call(
         _lib.sparse_qk_norm_rope, dev, stream, ctypes.byref(r), _rows(q, b, t, hq, "q"),
-        _rows(k, b, t, hk, "k"), _bf16(q_weight, 128, "q_weight"),
-        _bf16(k_weight, 128, "k_weight"), _i32(positions, b * t, "positions"),
-        _f32(table, r.table_rows * r.rotary_dim, "table"), _rows(q_out, b, t, hq, "q_out"),
+        _rows(k, b, t, hk, "k"), _flat(q_weight, _BF16, 128, "q_weight"),
+        _flat(k_weight, _BF16, 128, "k_weight"), _flat(positions, _I32, b * t, "positions"),
+        _flat(table, _F32, r.table_rows * r.rotary_dim, "table"), _rows(q_out, b, t, hq, "q_out"),
         _rows(k_out, b, t, hk, "k_out"), _word(error))
 
 
@@ -438,13 +438,13 @@ def sparse_paged_append(params: SpaPagedParams, rope: Optional[SpaRopeParams], q
     return _call(
         _lib.sparse_paged_append, dev, stream, ctypes.byref(p),
         None if rope is None else ctypes.byref(rope), _rows(q, 1, t, hq, "q"),
-        _rows(k, 1, t, hk, "k"), _rows(v, 1, t, hk, "v"), _bf16(q_weight, 128, "q_weight"),
-        _bf16(k_weight, 128, "k_weight"),
-        _f32(table, 0 if rope is None else rope.table_rows * rope.rotary_dim, "table"),
-        _i32(cu_q, seqs + 1, "cu_q"), _i32(kv_lens, seqs, "kv_lens"),
-        _i32(block_table, seqs * p.pages_per_seq, "block_table"), _rows(q_out, 1, t, hq, "q_out"),
+        _rows(k, 1, t, hk, "k"), _rows(v, 1, t, hk, "v"), _flat(q_weight, _BF16, 128, "q_weight"),
+        _flat(k_weight, _BF16, 128, "k_weight"),
+        _flat(table, _F32, 0 if rope is None else rope.table_rows * rope.rotary_dim, "table"),
+        _flat(cu_q, _I32, seqs + 1, "cu_q"), _flat(kv_lens, _I32, seqs, "kv_lens"),
+        _flat(block_table, _I32, seqs * p.pages_per_seq, "block_table"), _rows(q_out, 1, t, hq, "q_out"),
         _cache(p, k_cache, "k_cache"), _cache(p, v_cache, "v_cache"),
-        _bf16(summary, p.num_pages * hk * 256, "summary"), _word(error))
+        _flat(summary, _BF16, p.num_pages * hk * 256, "summary"), _word(error))
 
 
 def sparse_paged_workspace_bytes(params: SpaPagedParams) -> int:
@@ -464,9 +464,9 @@ def sparse_paged_select(params: SpaPagedParams, q, summary, cu_q, kv_lens, block
     wb = _nbytes(workspace) if workspace_bytes is None else int(workspace_bytes)
     return _call(
         _lib.sparse_paged_select, dev, stream, ctypes.byref(p), _rows(q, 1, t, p.heads_q, "q"),
-        _bf16(summary, p.num_pages * hk * 256, "summary"), _i32(cu_q, seqs + 1, "cu_q"),
-        _i32(kv_lens, seqs, "kv_lens"), _i32(block_table, seqs * p.pages_per_seq, "block_table"),
-        _i32(lists, t * hk * _list_width(p), "lists"), _i32(counts, t * hk, "counts"),
+        _flat(summary, _BF16, p.num_pages * hk * 256, "summary"), _flat(cu_q, _I32, seqs + 1, "cu_q"),
+        _flat(kv_lens, _I32, seqs, "kv_lens"), _flat(block_table, _I32, seqs * p.pages_per_seq, "block_table"),
+        _flat(lists, _I32, t * hk * _list_width(p), "lists"), _flat(counts, _I32, t * hk, "counts"),
         _ptr(workspace), wb, _word(error))
 
 
@@ -482,10 +482,10 @@ def sparse_paged_attn(params: SpaPagedParams, q, k_cache, v_cache, cu_q, kv_lens
     return _call(
         _lib.sparse_paged_attn, dev, stream, ctypes.byref(p), _rows(q, 1, t, hq, "q"),
         _cache(p, k_cache, "k_cache"), _cache(p, v_cache, "v_cache"),
-        _i32(cu_q, seqs + 1, "cu_q"), _i32(kv_lens, seqs, "kv_lens"),
-        _i32(block_table, seqs * p.pages_per_seq, "block_table"),
-        _i32(lists, t * hk * _list_width(p), "lists"), _i32(counts, t * hk, "counts"),
-        _rows(o, 1, t, hq, "o"), _f32(lse, t * hq, "lse"), _ptr(workspace), wb, _word(error))
+        _flat(cu_q, _I32, seqs + 1, "cu_q"), _flat(kv_lens, _I32, seqs, "kv_lens"),
+        _flat(block_table, _I32, seqs * p.pages_per_seq, "block_table"),
+        _flat(lists, _I32, t * hk * _list_width(p), "lists"), _flat(counts, _I32, t * hk, "counts"),
+        _rows(o, 1, t, hq, "o"), _flat(lse, _F32, t * hq, "lse"), _ptr(workspace), wb, _word(error))
 
 
 def sparse_paged_status(error, stream=None) -> int:

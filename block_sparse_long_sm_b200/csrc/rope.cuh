@@ -112,9 +112,19 @@ __device__ __forceinline__ NormWeights load_weights(const __nv_bfloat16* weight,
   return n;
 }
 
+__device__ __forceinline__ void rotate_halves(Row16& v, const Angles& a) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float e = v.x[i], o = v.x[8 + i];
+    v.x[i] = e * a.c[i] - o * a.s[i];
+    v.x[8 + i] = o * a.c[i] + e * a.s[i];
+  }
+}
+
 // Norm (of this row when `mine`; `any`, the same for the whole warp: of some
 // row) and rotation of the row held by the eight lanes; every lane of the warp
 // takes part (shuffles).  rsqrtf is off by at most 2 units in the last place of fp32.
+template <bool HALVES = false>   // rotation of all 128 dims in halves, known beforehand
 __device__ __forceinline__ void norm_rotate(Row16& v, bool any, bool mine, const NormWeights& n,
                                             const RopeSpec& r, const Angles& a, int li) {
   if (any) {
@@ -132,6 +142,10 @@ __device__ __forceinline__ void norm_rotate(Row16& v, bool any, bool mine, const
 #pragma unroll
     for (int i = 0; i < 8; ++i) v.x[8 + i] = v.x[8 + i] * f * w[i];
   }
+  if (HALVES) {
+    rotate_halves(v, a);
+    return;
+  }
   if (r.rot == 0) return;
   if (r.interleaved) {
     // lanes past rotary_dim hold c = 1, s = 0
@@ -142,12 +156,7 @@ __device__ __forceinline__ void norm_rotate(Row16& v, bool any, bool mine, const
       v.x[2 * i + 1] = o * a.c[i] + e * a.s[i];
     }
   } else if (r.rot == 128) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float e = v.x[i], o = v.x[8 + i];
-      v.x[i] = e * a.c[i] - o * a.s[i];
-      v.x[8 + i] = o * a.c[i] + e * a.s[i];
-    }
+    rotate_halves(v, a);
   } else {
     const int hl = r.rot >> 4;                  // lanes per half
     const float sign = (li & hl) ? 1.f : -1.f;  // second half: + s * first
@@ -178,11 +187,13 @@ constexpr int kRopeThreads = 256;
 
 // One warp: one token, heads_per_warp of its heads, four at a time.  The angles
 // are loaded once per warp (40 heads per warp instead of 20: 259 us instead of
-// 274 on 65536 tokens of 40 heads, 5.3 TB/s), the weights with every row (from
-// L1; kept in registers, in a loop per side, they cost more in loads under way
-// than they save: 299 us).  The rows of a step are independent, so the loop is
-// unrolled to keep several 16-byte loads per lane in flight, and four blocks
-// per SM bound the registers (with as many as the compiler likes: 291 us).
+// 274 on 65536 tokens of 40 heads), the weights with every row (from L1; kept in
+// registers, in a loop per side, they cost more in loads under way than they
+// save: 299 us).  The rows of a step are independent, so the loop is unrolled
+// to keep several 16-byte loads per lane in flight, and four blocks per SM bound
+// the registers (three: 271 us, five: 266 us).  The usual rotation, all 128 dims
+// in halves, has a kernel of its own: 243 us, 5.65 TB/s, against 259.
+template <bool HALVES>
 __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const NormRopeArgs a) {
   const long long w = (static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x) >> 5;
   if (w >= a.warps) return;
@@ -210,7 +221,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const NormRo
     unpack8(*reinterpret_cast<const uint4*>(src + 8 * li), v.x);
     unpack8(*reinterpret_cast<const uint4*>(src + 64 + 8 * li), v.x + 8);
     const __nv_bfloat16* weight = isq ? a.qw : a.kw;
-    norm_rotate(v, a.qw != nullptr || a.kw != nullptr, weight != nullptr,
+    norm_rotate<HALVES>(v, a.qw != nullptr || a.kw != nullptr, weight != nullptr,
                 load_weights(weight, li), a.r, ang, li);
     if (on) {
       __nv_bfloat16* dst = isq ? a.qo.at(b, t, hr) : a.ko.at(b, t, hr);

@@ -230,7 +230,10 @@ SPA_API spa_status sparse_qk_norm_rope(const spa_rope_params* r, const spa_rows*
   a.err = error_word;
   const long long blocks = (a.warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (blocks > INT_MAX) return SPA_ERR_UNSUPPORTED;
-  norm_rope_kernel<<<(unsigned)blocks, kRopeThreads, 0, stream>>>(a);
+  if (r->rotary_dim == 128 && !r->interleaved)
+    norm_rope_kernel<true><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(a);
+  else
+    norm_rope_kernel<false><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? SPA_OK : SPA_ERR_CUDA;
 }
 

@@ -162,11 +162,11 @@ def test_tensor_checks_of_the_binding():
     both = torch.zeros(8, 4, 16, 128, dtype=torch.bfloat16)
     assert binding._cache(paged(page_stride=4 * 16 * 128), both[:, 2:], "v") == both[:, 2:].data_ptr()
     with pytest.raises(ValueError):
-        binding._i32(torch.zeros(3, dtype=torch.int32), 4, "cu_q")
+        binding._flat(torch.zeros(3, dtype=torch.int32), torch.int32, 4, "cu_q")
     with pytest.raises(TypeError):
-        binding._i32(torch.zeros(4, dtype=torch.int64), 4, "cu_q")
+        binding._flat(torch.zeros(4, dtype=torch.int64), torch.int32, 4, "cu_q")
     with pytest.raises(ValueError):
-        binding._i32(torch.zeros(4, 2, dtype=torch.int32)[:, 0], 4, "cu_q")
+        binding._flat(torch.zeros(4, 2, dtype=torch.int32)[:, 0], torch.int32, 4, "cu_q")
     with pytest.raises(ValueError):                    # host memory
         spa.sparse_paged_status(torch.zeros(1, dtype=torch.int32), stream=0)
 
