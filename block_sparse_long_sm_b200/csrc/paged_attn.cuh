@@ -659,7 +659,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     tmem_relinquish();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // what the stream did before is visible
-  // this CTA's piece of the line
+  // this CTA's piece of the line: only the walking warp needs it, and finds it
+  // by itself when the sequences are few
   const int c = blockIdx.x;
   // pieces: none without a tile of a unit that spans it, so that every CTA
   // between the first and the last of a shared unit has a part of it
@@ -673,19 +674,28 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     f.total = static_cast<long long>(a.q.T) * a.Hkv * a.unit_length;
   } else {
     bool duo = false;
-    f = block_find(
-        a.q.S,
-        [&](int s) {
-          bool d;
-          const long long len = PagedWalk<LIST>::head_length(a, s, d) * a.Hkv;
-          duo |= d;
-          return len;
-        },
-        [&](long long total) {
-          any_duo = __syncthreads_or(duo);
+    auto length = [&](int s) {
+      bool d;
+      const long long len = PagedWalk<LIST>::head_length(a, s, d) * a.Hkv;
+      duo |= d;
+      return len;
+    };
+    if (a.q.S <= 32 * kWarpFind) {
+      if (warp == 10) {
+        f = warp_find(a.q.S, length, [&](long long total) {
+          any_duo = __any_sync(0xffffffffu, duo);
           return total * c / pieces(total);
-        },
-        find);
+        });
+      }
+    } else {
+      f = block_find(
+          a.q.S, length,
+          [&](long long total) {
+            any_duo = __syncthreads_or(duo);
+            return total * c / pieces(total);
+          },
+          find);
+    }
   }
   const int G = pieces(f.total);
   tc_fence_before();

@@ -160,4 +160,44 @@ __device__ __forceinline__ Found block_find(int S, Cost cost, Target target, Fin
   return f;
 }
 
+// The same by one warp, for up to 32 * kWarpFind sequences: all lengths are
+// read side by side, nothing waits for the block.
+constexpr int kWarpFind = 4;
+template <class Cost, class Target>
+__device__ __forceinline__ Found warp_find(int S, Cost cost, Target target) {
+  const int lane = threadIdx.x & 31;
+  long long c[kWarpFind], mine = 0;
+#pragma unroll
+  for (int k = 0; k < kWarpFind; ++k) {
+    const int s = kWarpFind * lane + k;
+    c[k] = s < S ? cost(s) : 0;
+    mine += c[k];
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  Found f;
+  f.total = __shfl_sync(0xffffffffu, incl, 31);
+  f.x = target(f.total);
+  long long at = incl - mine;
+  int hit = -1;
+  long long base = 0;
+#pragma unroll
+  for (int k = 0; k < kWarpFind; ++k) {
+    if (at <= f.x && f.x < at + c[k]) {
+      hit = kWarpFind * lane + k;
+      base = at;
+    }
+    at += c[k];
+  }
+  const uint32_t who = __ballot_sync(0xffffffffu, hit >= 0);
+  const int src = who ? __ffs(who) - 1 : 0;
+  f.s = __shfl_sync(0xffffffffu, hit, src);
+  f.base = __shfl_sync(0xffffffffu, base, src);
+  return f;
+}
+
 }  // namespace spa
