@@ -140,7 +140,7 @@ constexpr long long kPagedSlotFloats = 130LL * kPagedSlotRows;
 
 // The CTA whose piece [total * c / G, total * (c + 1) / G) holds point x.
 __device__ __forceinline__ int piece_of(long long x, long long total, int G) {
-  return static_cast<int>(((x + 1) * G - 1) / total);
+  return static_cast<int>(quotient((x + 1) * G - 1, total));
 }
 
 // ---------------------------------------------------------------------------
@@ -247,12 +247,12 @@ struct PagedWalk {
     }
   }
 
-  // Goes to the unit that holds x0.  s0, base0: the sequence that holds it and
-  // where that starts (not LIST).
-  __device__ __forceinline__ void start(int s0, long long base0) {
+  // Goes to the unit that holds x0.  s0, base0, length0: the sequence that holds
+  // it, where that starts and its length (not LIST).
+  __device__ __forceinline__ void start(int s0, long long base0, long long length0) {
     if (LIST) {
-      const long long u = x0 / a.unit_length;
-      s = static_cast<int>(u / a.Hkv);
+      const long long u = quotient(x0, a.unit_length);
+      s = static_cast<int>(quotient(u, a.Hkv));
       g = static_cast<int>(u - static_cast<long long>(s) * a.Hkv);
       base = u * a.unit_length;
       r = 0;
@@ -261,9 +261,8 @@ struct PagedWalk {
       s = s0;
       base = base0;
       load_seq();
-      bool duo;
-      const long long per_head = head_length(a, s, duo);
-      g = static_cast<int>((x0 - base0) / per_head);
+      const long long per_head = quotient(length0, a.Hkv);
+      g = static_cast<int>(quotient(x0 - base0, per_head));
       base += g * per_head;
       r = 0;
       while (true) {
@@ -324,8 +323,11 @@ struct PagedWalk {
       return ntok > 0;
     }
     const long long t0 = base + edge;
-    b = static_cast<int>((max(x0 - t0, 0LL) + w - 1) / w);
-    e = static_cast<int>(min((max(x1 - t0, 0LL) + w - 1) / w, static_cast<long long>(nt)));
+    const long long all = static_cast<long long>(nt) * w;          // below 2^32
+    const uint32_t p0 = static_cast<uint32_t>(min(max(x0 - t0, 0LL), all));
+    const uint32_t p1 = static_cast<uint32_t>(min(max(x1 - t0, 0LL), all));
+    b = static_cast<int>(w == kTileDuo ? (p0 + kTileDuo - 1) / kTileDuo : (p0 + kTileOne - 1) / kTileOne);
+    e = static_cast<int>(w == kTileDuo ? (p1 + kTileDuo - 1) / kTileDuo : (p1 + kTileOne - 1) / kTileOne);
     return b < e && ntok > 0;
   }
 };
@@ -669,7 +671,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     return static_cast<int>(
         min(static_cast<long long>(gridDim.x), max(total / (any_duo ? kTileDuo : kTileOne), 1LL)));
   };
-  Found f{0, 0, 0, 0};
+  Found f{0, 0, 0, 0, 0};
   if (LIST) {
     f.total = static_cast<long long>(a.q.T) * a.Hkv * a.unit_length;
   } else {
@@ -684,7 +686,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (warp == 10) {
         f = warp_find(a.q.S, length, [&](long long total) {
           any_duo = __any_sync(0xffffffffu, duo);
-          return total * c / pieces(total);
+          return quotient(total * c, pieces(total));
         });
       }
     } else {
@@ -692,7 +694,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           a.q.S, length,
           [&](long long total) {
             any_duo = __syncthreads_or(duo);
-            return total * c / pieces(total);
+            return quotient(total * c, pieces(total));
           },
           find);
     }
@@ -936,8 +938,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     } else if (warp == 10) {
       // ----------------------------------------------- the CTA's segments
       PagedWalk<LIST> walk(a);
-      walk.x0 = f.total * c / G;
-      walk.x1 = f.total * (c + 1) / G;
+      walk.x0 = LIST ? quotient(f.total * c, G) : f.x;
+      walk.x1 = quotient(f.total * (c + 1), G);
       if (LIST && a.whole_units) {
         walk.x0 = c;
         walk.x1 = static_cast<long long>(a.q.T) * a.Hkv;
@@ -982,7 +984,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         if (LIST && a.whole_units)
           walk.turn(walk.x0);
         else
-          walk.start(f.s, f.base);
+          walk.start(f.s, f.base, f.cost);
         for (; ok && walk.more(); walk.next()) {
           int tb, te;
           if (!walk.range(tb, te)) continue;

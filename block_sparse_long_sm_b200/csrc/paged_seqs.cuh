@@ -80,7 +80,7 @@ __device__ __forceinline__ int phys_page(const Seqs& v, int s, int j) {
 // ---------------------------------------------------------------------------
 struct FindSmem {
   long long warp_sums[32];
-  long long total, base;
+  long long total, base, cost;
   int s;
 };
 
@@ -88,7 +88,16 @@ struct Found {
   int s;             // -1: x is past the last sequence
   long long base;    // cost of the sequences before s
   long long total, x;
+  long long cost;    // of s
 };
+
+// Quotients of non-negative numbers that mostly fit into 32 bits (a 64-bit
+// division is some 150 cycles on the way to a kernel's first load).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 __device__ __forceinline__ long long block_exclusive_sum(long long c, FindSmem& sm) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -136,6 +145,7 @@ __device__ __forceinline__ Found block_find(int S, Cost cost, Target target, Fin
     if (excl <= x && x < excl + c) {
       sm.s = threadIdx.x;
       sm.base = excl;
+      sm.cost = c;
     }
   } else {
     long long run = 0;
@@ -147,6 +157,7 @@ __device__ __forceinline__ Found block_find(int S, Cost cost, Target target, Fin
       if (excl <= x && x < excl + c) {
         sm.s = s;
         sm.base = excl;
+        sm.cost = c;
       }
       __syncthreads();
     }
@@ -155,6 +166,7 @@ __device__ __forceinline__ Found block_find(int S, Cost cost, Target target, Fin
   Found f;
   f.s = sm.s;
   f.base = sm.s >= 0 ? sm.base : 0;
+  f.cost = sm.s >= 0 ? sm.cost : 0;
   f.total = total;
   f.x = x;
   return f;
@@ -184,12 +196,13 @@ __device__ __forceinline__ Found warp_find(int S, Cost cost, Target target) {
   f.x = target(f.total);
   long long at = incl - mine;
   int hit = -1;
-  long long base = 0;
+  long long base = 0, cost_hit = 0;
 #pragma unroll
   for (int k = 0; k < kWarpFind; ++k) {
     if (at <= f.x && f.x < at + c[k]) {
       hit = kWarpFind * lane + k;
       base = at;
+      cost_hit = c[k];
     }
     at += c[k];
   }
@@ -197,6 +210,7 @@ __device__ __forceinline__ Found warp_find(int S, Cost cost, Target target) {
   const int src = who ? __ffs(who) - 1 : 0;
   f.s = __shfl_sync(0xffffffffu, hit, src);
   f.base = __shfl_sync(0xffffffffu, base, src);
+  f.cost = __shfl_sync(0xffffffffu, cost_hit, src);
   return f;
 }
 
