@@ -38,6 +38,12 @@
 // page_top_kernel    one block per token and kv head: radix search of the
 //                    score of rank top_pages, the exact sums between, and one
 //                    scan that writes the kept pages in ascending order.
+// page_top_warp_kernel  the same by one warp, for up to 512 candidates: the score
+//                    of rank top_pages is found bit by bit, a count over the
+//                    warp each.  No barriers, and all of a chunk's tokens are
+//                    under way at once: 25 us instead of 37 for 2000 selections
+//                    among 506 pages.  (Among 2048 pages a warp takes 50 us, a
+//                    block 14.)
 #pragma once
 
 #include "paged_seqs.cuh"
@@ -503,6 +509,148 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     }
     gt += vd == 1;
     eq += vd == 2;
+  }
+}
+
+// The largest v with at least `rank` of the warp's keys at or above it, among
+// the bits below and at `bit` (v: the bits above); count(v) counts over the warp.
+template <class Count>
+__device__ __forceinline__ uint32_t bit_rank(uint32_t v, int bit, uint32_t rank, Count count) {
+  for (; bit >= 0; --bit) {
+    const uint32_t c = v | (1u << bit);
+    if (count(c) >= rank) v = c;
+  }
+  return v;
+}
+
+constexpr int kTopWarpThreads = 128;
+constexpr int kTopWarpKeys = 512;
+
+struct TopWarpSmem {
+  uint32_t keys[kTopWarpKeys];
+  uint32_t in[kTopWarpKeys / 32], band[kTopWarpKeys / 32];   // kept at once; between
+};
+
+__global__ void __launch_bounds__(kTopWarpThreads) page_top_warp_kernel(const SelectArgs a) {
+  __shared__ TopWarpSmem smem[kTopWarpThreads / 32];
+  const long long tg =
+      static_cast<long long>(blockIdx.x) * (kTopWarpThreads / 32) + (threadIdx.x >> 5);
+  if (tg >= static_cast<long long>(a.q.T) * a.Hkv) return;
+  const int t = static_cast<int>(tg / a.Hkv);
+  const int g = static_cast<int>(tg - static_cast<long long>(t) * a.Hkv);
+  const int lane = threadIdx.x & 31;
+  TopWarpSmem& sm = smem[threadIdx.x >> 5];
+  int s;
+  const Seq q = seq_of_token(a.q, t, s);
+  if (q.n == 0) return;
+  const Candidates cd = candidates(a, q.kv - q.n + (t - q.q0));
+  int32_t* out = a.lists + tg * a.width;
+  const int kept = min(cd.n, a.top);
+  const int head = min(a.sink, cd.seen);            // sink pages
+  const int tail = cd.seen - head - cd.n;           // recent pages
+  const int count = head + kept + tail;
+  if (lane == 0) a.counts[tg] = count;
+  for (int i = lane; i < a.width; i += 32) {
+    // everything but the chosen pages (all candidates when they fit)
+    if (i < head)
+      out[i] = i;
+    else if (i >= count)
+      out[i] = -1;
+    else if (i >= head + kept)
+      out[i] = cd.seen - (count - i);
+    else if (cd.n <= a.top)
+      out[i] = i;
+  }
+  if (cd.n <= a.top || a.top == 0) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the scores
+  const float2* score = a.score + tg * a.q.per_seq;
+  const int steps = (cd.n + 31) >> 5;               // candidate 32 k + lane; key 0: none
+  float big = 0.f;
+  uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll 8
+  for (int k = 0; k < steps; ++k) {
+    const bool on = 32 * k + lane < cd.n;
+    const float2 x = on ? score[32 * k + lane] : make_float2(0.f, 0.f);
+    const uint32_t u = on ? ordered(x.x) : 0u;
+    sm.keys[32 * k + lane] = u;
+    big = fmaxf(big, x.y);
+    lo = on ? min(lo, u) : lo;
+    hi = max(hi, u);
+  }
+  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  // bits above the highest one in which the keys differ are common to all; every
+  // lane reads only its own keys until the exact ones are written
+  const int bit = 31 - __clz(lo ^ hi);
+  const uint32_t edge =
+      bit_rank(bit >= 31 ? 0u : hi & ~((1u << (bit + 1)) - 1u), bit, a.top, [&](uint32_t c) {
+        uint32_t n = 0;
+#pragma unroll 8
+        for (int k = 0; k < steps; ++k) n += sm.keys[32 * k + lane] >= c;
+        return __reduce_add_sync(0xffffffffu, n);
+      });
+  // keys above `top` are kept, below `bottom` are not
+  const float e2 = big * (1.0f / 8192.0f), mid = unordered(edge);
+  const uint32_t top = ordered(mid + e2), bottom = max(1u, ordered(mid - e2));
+  uint32_t in = 0, between = 0;
+#pragma unroll 4
+  for (int k = 0; k < steps; ++k) {
+    const uint32_t u = sm.keys[32 * k + lane];
+    const uint32_t x = __ballot_sync(0xffffffffu, u > top);
+    const uint32_t y = __ballot_sync(0xffffffffu, u <= top && u >= bottom);
+    in += __popc(x);
+    between += __popc(y);
+    if (lane == 0) {
+      sm.in[k] = x;
+      sm.band[k] = y;
+    }
+  }
+  __syncwarp();
+  const uint32_t need = a.top - in;                 // of those between; at least one
+  const bool ranked = between > need;
+  uint32_t least = 0u, equal = 0xffffffffu;         // of the pages between, when ranked
+  if (ranked) {
+    uint32_t elo = 0xffffffffu, ehi = 0u;
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) {
+      uint32_t todo = sm.band[k];
+#pragma unroll 1
+      while (todo) {
+        const int i = 32 * k + __ffs(todo) - 1;
+        todo &= todo - 1;
+        const uint32_t x = ordered(exact_score(a, s, t, g, i));
+        if (lane == 0) sm.keys[i] = x;
+        elo = min(elo, x);
+        ehi = max(ehi, x);
+      }
+    }
+    __syncwarp();
+    const int eb = 31 - __clz(elo ^ ehi);
+    auto over = [&](uint32_t c) {
+      uint32_t n = 0;
+#pragma unroll 4
+      for (int k = 0; k < steps; ++k)
+        n += ((sm.band[k] >> lane) & 1u) && sm.keys[32 * k + lane] >= c;
+      return __reduce_add_sync(0xffffffffu, n);
+    };
+    least = bit_rank(eb >= 31 ? 0u : ehi & ~((1u << (eb + 1)) - 1u), eb, need, over);
+    equal = need - (least == 0xffffffffu ? 0u : over(least + 1u));
+  }
+  uint32_t at = 0, eq = 0;
+  const uint32_t before = (1u << lane) - 1u;
+#pragma unroll 2
+  for (int k = 0; k < steps; ++k) {
+    const uint32_t u = sm.keys[32 * k + lane], band = sm.band[k];
+    const bool mine = (band >> lane) & 1u;
+    const uint32_t ties = __ballot_sync(0xffffffffu, ranked && mine && u == least);
+    bool keep = (sm.in[k] >> lane) & 1u;
+    if (mine) keep = !ranked || u > least || (u == least && eq + __popc(ties & before) < equal);
+    const uint32_t all = __ballot_sync(0xffffffffu, keep);
+    const uint32_t pos = at + __popc(all & before);
+    if (keep && pos < static_cast<uint32_t>(a.top)) out[head + pos] = a.sink + 32 * k + lane;
+    at += __popc(all);
+    eq += __popc(ties);
   }
 }
 

@@ -158,10 +158,10 @@ spa_status paged_checks(const spa_paged_params* p, const spa_rows* q, const int3
   return SPA_OK;
 }
 
-// Launch that may begin before the stream's previous kernel has ended; the
-// kernel itself waits for that one's results.
+// Launch that, with `early`, may begin before the stream's previous kernel has
+// ended; the kernel itself waits for that one's results.
 template <typename... P, typename... A>
-bool launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+bool launch_after(bool early, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
                   cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -172,7 +172,7 @@ bool launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
@@ -180,11 +180,11 @@ template <bool LIST>
 bool launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                   const PagedAttnArgs& a, int combine_y, cudaStream_t stream) {
   if (set_smem(paged_attn_kernel<LIST>, kPagedSmemBytes) != cudaSuccess) return false;
-  if (!launch_after(paged_attn_kernel<LIST>, dim3(kPagedGrid), kPagedThreads, kPagedSmemBytes,
+  if (!launch_after(true, paged_attn_kernel<LIST>, dim3(kPagedGrid), kPagedThreads, kPagedSmemBytes,
                     stream, tq, tk, tv, a))
     return false;
   if (a.whole_units) return true;
-  return launch_after(paged_combine_kernel, dim3(kPagedGrid, combine_y), kCombineThreads, 0,
+  return launch_after(true, paged_combine_kernel, dim3(kPagedGrid, combine_y), kCombineThreads, 0,
                       stream, a);
 }
 
@@ -326,21 +326,27 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
   const long long most = (long long)p->pages_per_seq - a.sink - a.local;   // candidates
   const long long tg = (long long)p->tokens * p->heads_kv;
   if (tg > INT_MAX) return SPA_ERR_UNSUPPORTED;
-  if (set_smem(page_top_kernel, top_smem_bytes(INT_MAX)) != cudaSuccess) return SPA_ERR_CUDA;
-  if (most > a.top && a.top > 0) {
+  const bool scored = most > a.top && a.top > 0;
+  if (scored) {
+    const long long groups = ((long long)p->tokens + a.tm - 1) / a.tm * p->heads_kv;
     a.chunks = (int)((most + kScorePages - 1) / kScorePages);
-    const long long blocks = ((long long)p->tokens + a.tm - 1) / a.tm * p->heads_kv * a.chunks;
+    const long long blocks = groups * a.chunks;
     if (blocks > INT_MAX) return SPA_ERR_UNSUPPORTED;
     page_score_kernel<<<(unsigned)blocks, kScoreThreads, 0, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPA_ERR_CUDA;
-    // (begins while the scores are computed: it reads the lengths meanwhile)
-    return launch_after(page_top_kernel, dim3((unsigned)tg), kTopThreads,
-                        top_smem_bytes(p->pages_per_seq), stream, a)
-               ? SPA_OK
-               : SPA_ERR_CUDA;
   }
-  page_top_kernel<<<(unsigned)tg, kTopThreads, top_smem_bytes(p->pages_per_seq), stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SPA_OK : SPA_ERR_CUDA;
+  // (begins while the scores are computed: it reads the lengths meanwhile)
+  const unsigned warp_blocks = (unsigned)((tg + kTopWarpThreads / 32 - 1) / (kTopWarpThreads / 32));
+  bool ok;
+  if (most > kTopWarpKeys) {
+    if (set_smem(page_top_kernel, top_smem_bytes(INT_MAX)) != cudaSuccess) return SPA_ERR_CUDA;
+    ok = launch_after(scored, page_top_kernel, dim3((unsigned)tg), kTopThreads,
+                      top_smem_bytes(p->pages_per_seq), stream, a);
+  } else {
+    ok = launch_after(scored, page_top_warp_kernel, dim3(warp_blocks), kTopWarpThreads, 0, stream,
+                      a);
+  }
+  return ok ? SPA_OK : SPA_ERR_CUDA;
 }
 
 SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* q,

@@ -135,3 +135,26 @@ def test_many_tokens_take_whole_units_in_turn():
     o, lse = attend(b, p, lists, counts, ws=ws)
     check_attention(b, o, lse, pages_of=lambda t, g: want[(t, g)], rows=pick)
     b.ok()
+
+
+@pytest.mark.parametrize("pages,top", [(256, 9), (515, 100), (516, 1), (516, 511), (515, 511),
+                                       (1030, 700), (2051, 2047)])
+def test_candidate_counts_around_the_kernels_limits(pages, top):
+    b = Batch(8, 2, 16, [(1, 16 * pages - 3), (1, 40)], seed=pages)
+    _, sm, lists, counts, _ = run_select(b, 1, 2, top)
+    check_lists(b, lists, counts, expected(b, sm, 1, 2, top))
+    b.ok()
+
+
+@pytest.mark.parametrize("pages", [200, 900, 1900])
+def test_ties_at_the_border_of_every_size(pages):
+    b = Batch(2, 1, 16, [(1, 16 * pages)], seed=1)
+    rng = np.random.default_rng(pages)
+    kinds = bits_of(rng.standard_normal((4, 2, D)))
+    kinds[:, 1] = bits_of(np.maximum(f64(kinds[:, 0]), f64(kinds[:, 1])))
+    sm = b.summary()
+    for j in range(pages):
+        sm[b.table[0, j], 0] = kinds[rng.integers(0, 4)]
+    for top in (pages // 7, pages // 2, pages - 3):
+        _, _, lists, counts, _ = run_select(b, 1, 1, top, summary=sm)
+        check_lists(b, lists, counts, expected(b, sm, 1, 1, top))
