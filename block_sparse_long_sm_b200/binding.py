@@ -326,15 +326,22 @@ def _rows(x, batch, tokens, heads, name):
         return None
     if x.__class__ is SpaRows:
         return ctypes.byref(x)
-    sh, st = x.shape, x.stride()
-    if sh[-3:] != (tokens, heads, 128) or (sh[0] != batch if len(sh) == 4 else batch != 1) \
-            or not 3 <= len(sh) <= 4:
-        raise ValueError(f"{name}: shape {tuple(sh)}, wanted {(batch, tokens, heads, 128)}")
+    st = x.stride()
+    if len(st) == 3 and batch == 1:
+        good, sb = x.shape == (tokens, heads, 128), 0
+        s_t, s_h, s_d = st
+    elif len(st) == 4:
+        good = x.shape == (batch, tokens, heads, 128)
+        sb, s_t, s_h, s_d = st
+    else:
+        good = False
+    if not good:
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted {(batch, tokens, heads, 128)}")
     if x.dtype is not _BF16:
         raise TypeError(f"{name}: {x.dtype}, wanted torch.bfloat16")
-    if st[-1] != 1 and x.numel():
+    if s_d != 1 and x.numel():
         raise ValueError(f"{name}: the 128 elements of a row have to be contiguous")
-    return ctypes.byref(SpaRows(x.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2]))
+    return ctypes.byref(SpaRows(x.data_ptr(), sb, s_t, s_h))
 
 
 def _flat(x, dtype, count, name):
