@@ -409,7 +409,7 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
   // rows by a quarter of the columns)
   long long rows = lists ? group : (long long)p->tokens * group / p->seqs;
   if (rows > kPagedSlotRows) rows = kPagedSlotRows;
-  const int cy = rows > 8 ? (int)(rows + 7) / 8 : 1;
+  const int cy = rows > 16 ? (int)(rows + 15) / 16 : 1;
   const bool ok = lists ? launch_paged<true>(tq, tk, tv, a, cy, stream)
                         : launch_paged<false>(tq, tk, tv, a, cy, stream);
   return ok ? SPA_OK : SPA_ERR_CUDA;
