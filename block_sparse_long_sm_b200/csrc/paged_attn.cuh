@@ -33,20 +33,29 @@
 // A step batch that mixes prompt chunks and single tokens has both.
 //
 // Work split.  All (sequence, kv head, row tiles) units lie end to end on one
-// line, as long as they take, and each CTA (one per SM, persistent) takes an equal piece of
-// that line, found by a scan over the sequences' lengths: every SM has the same
-// work however ragged the batch is, one long sequence included.  A unit that one CTA covers is finished there; the pieces
-// of the others (at most two per CTA) go to the workspace in fp32 and
-// paged_combine_kernel joins them in the order of their CTAs, so that the
-// result does not depend on timing.
+// line, as long as they take, and each CTA (one per SM, persistent) takes an
+// equal piece of that line, found by a scan over the sequences' lengths: every
+// SM has the same work however ragged the batch is, one long sequence included.
+// A unit that one CTA covers is finished there; the pieces of the others (at
+// most two per CTA) go to the workspace in fp32 and paged_combine_kernel joins
+// them in the order of their CTAs, so that the result does not depend on
+// timing.  Lists of many tokens are cut into whole units instead (see turn).
 //
 // Rows of V past the last visible key of a tile (the unfilled end of a page,
 // pages not loaded) are cleared before they are read: their probability is 0,
 // but 0 * NaN is not.
 //
 // Roles (384 threads): warps 0-3 / 4-7 softmax of slot 0 / 1, warp 8 loads,
-// warp 9 MMA, TMEM and the ends of V tiles, warp 10 walks the CTA's piece and hands its segments to the others through a ring of four, so
-// that the lengths and lists of the next units are read ahead.
+// warp 9 MMA, TMEM and the ends of V tiles, warp 10 walks the CTA's piece and
+// hands its segments to the others through a ring of four, so that the lengths,
+// lists and page numbers of the next units are read ahead.
+//
+// Measured (one B200; bound): 2048 tokens at 32K, 32/8 heads, 1.04-1.12 ms, 950
+// to 1026 TFLOP/s (the way of a tile's scores through its warpgroup: tensor
+// pipe busy for 2048 of some 3600 cycles per pair of tiles); one token at 128K,
+// 64/8 heads, 93 us, 5.8 TB/s, and 32 tokens of 300 to 16K keys 128 us, 5.5
+// TB/s (memory); one token at 1000 keys 12 us (latency of two kernels).
+//
 // TMEM columns: S_0 [0,128) (P_0 in [0,64)), S_1 [128,256), O_0 [256,384),
 // O_1 [384,512).
 #pragma once
@@ -122,6 +131,7 @@ struct PagedAttnArgs {
   int width;                 // list entries per (token, kv head)
   int unit_length;           // length on the line of a full list
   int whole_units;           // lists: CTAs take whole units in turn
+  int q_by_rows;             // q's heads lie further apart than its tokens
   int Hq, Hkv, group;
   int tpt1;                  // tokens per 128-row tile
   int pitch;                 // 128-element rows between pages
@@ -747,10 +757,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
             qlast[buf] = -1;
             continue;
           }
-          // one box of whole tokens per 64 columns; the rows behind the unit's last
-          // token are other tokens' or zero, and their results are not stored
-          if (lane == 0) {
-            const int tok = sg.tok0 + (duo ? buf * a.tpt1 : 0);
+          const int tok = sg.tok0 + (duo ? buf * a.tpt1 : 0);
+          if (a.q_by_rows) {
+            const int rows = min(a.tpt1, sg.ntok - (duo ? buf * a.tpt1 : 0)) * a.group;
+            if (lane == 0) mbar_arrive_expect_tx(bars.qfull(buf), rows * 256u);
+            __syncwarp();
+            for (int k = lane; k < rows; k += 32) {
+              const int ti = k / a.group, head = sg.g * a.group + (k - ti * a.group);
+              tma_load_3d(s_q(buf) + k * 128u, &tm_q, bars.qfull(buf), 0, tok + ti, head);
+              tma_load_3d(s_q(buf) + kHalfBytes + k * 128u, &tm_q, bars.qfull(buf), 64, tok + ti,
+                          head);
+            }
+          } else if (lane == 0) {
+            // one box of whole tokens per 64 columns; the rows behind the unit's
+            // last token are other tokens' or zero, and their results are not stored
             mbar_arrive_expect_tx(bars.qfull(buf), a.tpt1 * a.group * 256u);
             tma_load_3d(s_q(buf), &tm_q, bars.qfull(buf), 0, sg.g * a.group, tok);
             tma_load_3d(s_q(buf) + kHalfBytes, &tm_q, bars.qfull(buf), 64, sg.g * a.group, tok);

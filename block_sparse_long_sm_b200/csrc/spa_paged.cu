@@ -366,10 +366,15 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
   if ((reinterpret_cast<uintptr_t>(lists) & 3u) || (reinterpret_cast<uintptr_t>(counts) & 3u) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u))
     return SPA_ERR_INVALID;
-  // the q tensor map takes positive strides only
-  if (q->stride_token < 0 || q->stride_head < 0 || q->stride_token >= (1LL << 38) ||
-      q->stride_head >= (1LL << 38))
-    return SPA_ERR_UNSUPPORTED;
+  // The q tensor map wants positive strides, the larger a multiple of the
+  // smaller.  Tokens further apart than heads: boxes of whole tokens; the other
+  // way round (head-major rows): row by row.
+  long long sh = q->stride_head, st_q = q->stride_token;
+  if (p->heads_q == 1) sh = p->tokens == 1 ? 128 : st_q;
+  if (p->tokens == 1) st_q = sh;
+  if (sh <= 0 || st_q <= 0 || sh >= (1LL << 38) || st_q >= (1LL << 38)) return SPA_ERR_UNSUPPORTED;
+  const bool by_rows = st_q < sh;
+  if ((by_rows ? sh % st_q : st_q % sh) != 0) return SPA_ERR_UNSUPPORTED;
   const int group = p->heads_q / p->heads_kv;
   PagedAttnArgs a;
   a.q = seqs_of(p, cu_q, kv_lens, block_table, error_word);
@@ -384,6 +389,7 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
   // Eight or more units per CTA: whole ones in turn (the last round costs at
   // most an eighth, and nothing is left to join).
   a.whole_units = lists && (long long)p->tokens * p->heads_kv >= 8LL * kPagedGrid;
+  a.q_by_rows = by_rows;
   a.Hq = p->heads_q;
   a.Hkv = p->heads_kv;
   a.group = group;
@@ -400,8 +406,10 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
   const uint64_t cache_rows =
       (uint64_t)a.pitch * (p->num_pages - 1) + (uint64_t)p->heads_kv * p->page_size;
   CUtensorMap tq, tk, tv;
-  if (!map_rows(&tq, q->data, p->heads_q, p->tokens, q->stride_head, q->stride_token, group,
-                a.tpt1) ||
+  const bool q_map =
+      by_rows ? map_rows(&tq, q->data, p->tokens, p->heads_q, st_q, sh, 1, 1)
+              : map_rows(&tq, q->data, p->heads_q, p->tokens, sh, st_q, group, a.tpt1);
+  if (!q_map ||
       !map_2d(&tk, kBF16, 2, k_cache, 128, cache_rows, 64, p->page_size, kSW128) ||
       !map_2d(&tv, kBF16, 2, v_cache, 128, cache_rows, 64, p->page_size, kSW128))
     return SPA_ERR_CUDA;

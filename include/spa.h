@@ -458,7 +458,10 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
  * own: all of them, or with lists and counts (as sparse_paged_select writes
  * them, or the caller's own: ascending visible page numbers) those of the
  * listed pages.  o: bf16 rows like q; lse: optional fp32 [tokens][heads_q]
- * (natural log).  A token without keys gets o = 0, lse = -inf. */
+ * (natural log).  A token without keys gets o = 0, lse = -inf.  The strides of q
+ * have to be positive, the larger of token and head stride a multiple of the
+ * smaller (tokens outside heads, the usual way, is the faster); those of o are
+ * free.  o must not overlap q. */
 SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* q,
                                      const void* k_cache, const void* v_cache,
                                      const int32_t* cu_q, const int32_t* kv_lens,

@@ -181,6 +181,15 @@ def test_strided_queries_and_outputs():
     b.ok()
 
 
+@pytest.mark.parametrize("hq,hkv,seqs", [(6, 2, [(1, 500), (70, 130), (200, 260)]), (1, 1, [(300, 400)]),
+                                         (20, 1, [(9, 300), (1, 40)]), (4, 4, [(1, 99)])])
+def test_head_major_queries(hq, hkv, seqs):
+    b = Batch(hq, hkv, 32, seqs, seed=5)
+    q = b.q.transpose(0, 1).contiguous().transpose(0, 1)      # as the prefill lays them out
+    check_attention(b, *attend(b, q=q))
+    b.ok()
+
+
 def test_offsets_past_32_bits():
     # 24 pages 128 M elements apart: the last ones start past 2^31 elements (2^32 bytes)
     hq, hkv, page, n_pages, stride = 4, 2, 64, 24, 1 << 27

@@ -73,7 +73,10 @@ def test_workspace_is_closed_form_and_covers_its_parts():
     (dict(q=spa.SpaRows(A + 8, 0, 128, 128)), spa.SPA_ERR_INVALID),
     (dict(q=spa.SpaRows(A, 0, 4, 128)), spa.SPA_ERR_INVALID),
     (dict(q=spa.SpaRows(A, 0, 128, 130)), spa.SPA_ERR_INVALID),
-    (dict(q=spa.SpaRows(A, 0, -128, 128)), spa.SPA_ERR_UNSUPPORTED)])
+    (dict(q=spa.SpaRows(A, 0, -128, 128)), spa.SPA_ERR_UNSUPPORTED),
+    (dict(q=spa.SpaRows(A, 0, 0, 128)), spa.SPA_ERR_UNSUPPORTED),
+    (dict(q=spa.SpaRows(A, 0, 384, 256)), spa.SPA_ERR_UNSUPPORTED),
+    (dict(q=spa.SpaRows(A, 0, 256, 384)), spa.SPA_ERR_UNSUPPORTED)])
 def test_attn_and_select_arguments(kw, code):
     assert attn(paged(), **kw) == code
     if code != spa.SPA_ERR_UNSUPPORTED:
