@@ -1323,7 +1323,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
 // record of CTA x.  O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.  A warp
 // has four rows by 32 columns, a lane four columns of a row; the (m, l, O) of
 // eight pieces are read side by side (a serial merge took 17 us for 8 pieces of
-// one token).
+// one token).  Bound by the partials of 133 KB per slot, from L2: 24 us of the
+// 1.04 ms of 2048 tokens at 32K, 5 to 7 us for single tokens.
 constexpr int kCombineThreads = 256;
 constexpr int kCombinePieces = 8;
 

@@ -34,10 +34,14 @@
 //                    read 16-byte pieces of it (the order of a dot product's
 //                    terms is free, so the pieces are the matrix operand as
 //                    they come).  Tokens of one sequence that fit into the
-//                    sixteen rows share the loads.
+//                    sixteen rows share the loads.  16 sequences of up to 32K in
+//                    pages of 16: 50 MB of summaries, 22 us (2.3 TB/s); 250 tokens
+//                    that share 6 MB: 32 us (loads from L2, three products a page).
 // page_top_kernel    one block per token and kv head: radix search of the
 //                    score of rank top_pages, the exact sums between, and one
-//                    scan that writes the kept pages in ascending order.
+//                    scan that writes the kept pages in ascending order.  Bound
+//                    by latency, a dozen barriers and the loads between: 14 us for
+//                    one token among 2042 pages, 21 us for 16 tokens.
 // page_top_warp_kernel  the same by one warp, for up to 512 candidates: the score
 //                    of rank top_pages is found bit by bit, a count over the
 //                    warp each.  No barriers, and all of a chunk's tokens are

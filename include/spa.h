@@ -422,8 +422,8 @@ SPA_API spa_status sparse_qk_norm_rope(const spa_rope_params* r, const spa_rows*
  * (q_weight) and rotation; both NULL to leave them out.
  * summary: optional, bf16 [num_pages][heads_kv][2][128]; the minimum and the
  * maximum over the filled rows of every page that received a row are written
- * (other pages' entries are left as they are).  Two sequences may not write to
- * the same page in one call. */
+ * (other pages' entries are left as they are).  A page may receive rows through
+ * one table entry only in one call. */
 SPA_API spa_status sparse_paged_append(const spa_paged_params* p, const spa_rope_params* r,
                                        const spa_rows* q, const spa_rows* k, const spa_rows* v,
                                        const void* q_weight, const void* k_weight,
