@@ -50,6 +50,7 @@ __device__ __forceinline__ int append_segments(const Seqs& v, int s) {
 // 19.7 us, six 17.7 us); one token each of 64 sequences takes 5.6 us.  Bound by
 // the way of a block: lengths, table, rows, summary.
 __global__ void __launch_bounds__(kAppendThreads, 5) paged_append_kernel(const AppendArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the attention waits by itself
   const int lane = threadIdx.x & 31, li = lane & 7, warp = threadIdx.x >> 5;
   const Seqs& v = a.q;
   if (blockIdx.x >= a.kv_blocks) {

@@ -74,6 +74,8 @@ constexpr int kScorePages = kWarpPages * kScoreThreads / 32;
 constexpr int kTopThreads = 256;
 constexpr int kTopKeys = 16384;          // scores kept in shared memory
 constexpr int kTopBand = 256;            // pages ranked exactly there
+constexpr int kTopSteps = 8;             // keys of a thread, when they fit
+constexpr int kTopHeld = kTopSteps * kTopThreads;
 
 // Visible pages of a token and the candidates [sink, sink + n) among them.
 struct Candidates {
@@ -210,7 +212,7 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, const Seq& q, i
 // Block: tm token rows, one kv head, kScorePages candidates.  Rows of several
 // sequences are taken one sequence after the other.
 __global__ void __launch_bounds__(kScoreThreads, 3) page_score_kernel(const SelectArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // page_top waits by itself
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the ranking waits by itself
   // scores of one n8 group: [row][page], [row][page] of the magnitudes
   __shared__ float tile[kScoreThreads / 32][2][16][9];
   const long long bg = blockIdx.x / a.chunks;
@@ -236,11 +238,14 @@ __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
 
+static_assert(kTopBand == kTopThreads && kTopThreads == 256, "a thread per page between, eight warps");
 struct TopSmem {
   uint32_t band[kTopBand], exact[kTopBand], band_n;
+  int phys[kTopBand];
   uint32_t hist[256];
   uint32_t red[3][kTopThreads / 32];
   uint32_t found[2];
+  uint32_t count[2][2][kTopThreads / 32];
   unsigned long long sums[kTopThreads / 32];
   uint32_t keys[1];                      // [cap]: as many as pages_per_seq, up to kTopKeys
 };
@@ -325,36 +330,47 @@ __device__ __forceinline__ uint32_t radix_rank(int n, Key key, Use use, uint32_t
   return prefix + lo;
 }
 
-// Score of candidate i in 64 bits, rounded once: by a warp.
-__device__ __forceinline__ float exact_score(const SelectArgs& a, int s, int t, int g, int i) {
+// Score of the candidate in physical page `phys` in 64 bits, rounded once: by a
+// warp, four heads side by side.
+__device__ __forceinline__ float exact_score(const SelectArgs& a, int t, int g, int phys) {
   const int lane = threadIdx.x & 31;
-  int phys = phys_page(a.q, s, a.sink + i);
-  if (phys < 0) phys = 0;
   const uint2* pg = reinterpret_cast<const uint2*>(
-      a.summary + (static_cast<long long>(phys) * a.Hkv + g) * 256);
+      a.summary + (static_cast<long long>(max(phys, 0)) * a.Hkv + g) * 256);
   const uint2 l2 = pg[lane], h2 = pg[32 + lane];
   const float lo[4] = {__uint_as_float(l2.x << 16), __uint_as_float(l2.x & 0xffff0000u),
                        __uint_as_float(l2.y << 16), __uint_as_float(l2.y & 0xffff0000u)};
   const float hi[4] = {__uint_as_float(h2.x << 16), __uint_as_float(h2.x & 0xffff0000u),
                        __uint_as_float(h2.y << 16), __uint_as_float(h2.y & 0xffff0000u)};
   double best = -INFINITY;
-#pragma unroll 2
-  for (int h = 0; h < a.group; ++h) {
-    const uint2 q2 = reinterpret_cast<const uint2*>(a.xq.at(0, t, g * a.group + h))[lane];
-    const float qd[4] = {__uint_as_float(q2.x << 16), __uint_as_float(q2.x & 0xffff0000u),
-                         __uint_as_float(q2.y << 16), __uint_as_float(q2.y & 0xffff0000u)};
-    double sum = 0.0;
+#pragma unroll 1
+  for (int h0 = 0; h0 < a.group; h0 += 4) {
+    uint2 q2[4];
+    double sum[4];
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
-      sum += static_cast<double>(qd[d]) * static_cast<double>(qd[d] >= 0.f ? hi[d] : lo[d]);
+    for (int k = 0; k < 4; ++k)                     // (past the group: its last head again)
+      q2[k] = reinterpret_cast<const uint2*>(
+          a.xq.at(0, t, g * a.group + min(h0 + k, a.group - 1)))[lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    best = fmax(best, sum);
+    for (int k = 0; k < 4; ++k) {
+      const float qd[4] = {__uint_as_float(q2[k].x << 16), __uint_as_float(q2[k].x & 0xffff0000u),
+                           __uint_as_float(q2[k].y << 16), __uint_as_float(q2[k].y & 0xffff0000u)};
+      sum[k] = 0.0;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        sum[k] += static_cast<double>(qd[d]) * static_cast<double>(qd[d] >= 0.f ? hi[d] : lo[d]);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) best = fmax(best, sum[k]);
   }
   return static_cast<float>(best);
 }
 
 __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the attention waits by itself
   extern __shared__ __align__(16) uint8_t top_smem[];
   TopSmem& sm = *reinterpret_cast<TopSmem*>(top_smem);
   const long long tg = blockIdx.x;
@@ -363,7 +379,10 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int s;
   const Seq q = seq_of_token(a.q, t, s);
-  if (q.n == 0) return;
+  if (q.n == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // not done before the kernel before
+    return;
+  }
   const Candidates cd = candidates(a, q.kv - q.n + (t - q.q0));
   int32_t* out = a.lists + tg * a.width;
   const int kept = min(cd.n, a.top);
@@ -382,33 +401,117 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     else if (cd.n <= a.top)
       out[i] = i;
   }
-  if (cd.n <= a.top || a.top == 0) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the scores
+  if (cd.n <= a.top || a.top == 0) return;
   if (tid == 0) sm.band_n = 0;
   const int cap = top_keys(a.q.per_seq);
   float2* score = a.score + tg * a.q.per_seq;
   float big = 0.f;
-  for (int i = tid; i < cd.n; i += kTopThreads) {
-    const float2 x = score[i];
+  uint32_t least_key = 0xffffffffu, most_key = 0u;
+  const bool few = cd.n <= kTopHeld;                // keys stay in registers
+  uint32_t held[kTopSteps];
+  auto note = [&](const float2& x) {
+    const uint32_t u = ordered(x.x);
     big = fmaxf(big, x.y);
-    if (i < cap) sm.keys[i] = ordered(x.x);
+    least_key = min(least_key, u);
+    most_key = max(most_key, u);
+    return u;
+  };
+  if (few) {
+    float2 x[kTopSteps];
+#pragma unroll
+    for (int k = 0; k < kTopSteps; ++k)
+      if (tid + k * kTopThreads < cd.n) x[k] = score[tid + k * kTopThreads];
+#pragma unroll
+    for (int k = 0; k < kTopSteps; ++k) {
+      held[k] = 0u;                                 // below every point of the search
+      if (tid + k * kTopThreads < cd.n) {
+        held[k] = note(x[k]);
+        sm.keys[tid + k * kTopThreads] = held[k];
+      }
+    }
+  } else {
+#pragma unroll 4
+    for (int i = tid; i < cd.n; i += kTopThreads) {
+      const uint32_t u = note(score[i]);
+      if (i < cap) sm.keys[i] = u;
+    }
   }
   big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-  if (lane == 0) sm.red[2][warp] = __float_as_uint(big);
+  least_key = __reduce_min_sync(0xffffffffu, least_key);
+  most_key = __reduce_max_sync(0xffffffffu, most_key);
+  if (lane == 0) {
+    sm.red[0][warp] = least_key;
+    sm.red[1][warp] = most_key;
+    sm.red[2][warp] = __float_as_uint(big);
+  }
   __syncthreads();
+  least_key = __reduce_min_sync(0xffffffffu, sm.red[0][lane & (kTopThreads / 32 - 1)]);
+  most_key = __reduce_max_sync(0xffffffffu, sm.red[1][lane & (kTopThreads / 32 - 1)]);
   big = __uint_as_float(
       __reduce_max_sync(0xffffffffu, sm.red[2][lane & (kTopThreads / 32 - 1)]));
   auto key = [&](int i) { return i < cap ? sm.keys[i] : ordered(score[i].x); };
+  // The key of rank `top` lies in [first, last].  That interval is cut until it is
+  // no wider than the error of two sums; more would narrow the pages between only
+  // a little (26.4 us for one token, 26.8 us with an interval of a sixteenth of that).
+  const float e2 = big * (1.0f / 8192.0f);
   uint32_t rank = a.top;
-  uint32_t edge = radix_rank(cd.n, key, [](int) { return true; }, rank, sm);
+  uint32_t first = least_key, last = most_key;
+  if (few) {
+    int turn = 0;
+    while (first < last && !(unordered(last) - unordered(first) <= e2)) {
+      // three points, all within it, cut the interval into four
+      const uint32_t quarter = (last - first) >> 2;
+      const uint32_t p1 = first + quarter + 1u, p2 = p1 + quarter, p3 = p2 + quarter;
+      uint32_t n1 = 0, n23 = 0;                     // keys at or above them
+#pragma unroll
+      for (int k = 0; k < kTopSteps; ++k) {
+        n1 += held[k] >= p1;
+        n23 += (held[k] >= p2 ? 1u : 0u) + (held[k] >= p3 ? 0x10000u : 0u);
+      }
+      n1 = __reduce_add_sync(0xffffffffu, n1);
+      n23 = __reduce_add_sync(0xffffffffu, n23);
+      if (lane == 0) {
+        sm.count[turn][0][warp] = n1;
+        sm.count[turn][1][warp] = n23;
+      }
+      __syncthreads();                              // the counts of the step before are free
+      const uint32_t x = lane < 2 * (kTopThreads / 32)
+                             ? sm.count[turn][lane >> 3][lane & 7] : 0u;
+      n1 = __reduce_add_sync(0xffffffffu, lane < 8 ? x : 0u);
+      n23 = __reduce_add_sync(0xffffffffu, lane < 8 ? 0u : x);
+      turn ^= 1;
+      if ((n23 >> 16) >= rank) {
+        first = p3;
+      } else if ((n23 & 0xffffu) >= rank) {
+        first = p2;
+        last = p3 - 1u;
+      } else if (n1 >= rank) {
+        first = p1;
+        last = p2 - 1u;
+      } else {
+        last = p1 - 1u;
+      }
+    }
+  } else {
+    first = last = radix_rank(cd.n, key, [](int) { return true; }, rank, sm);
+  }
   // keys above `top` are kept, below `bottom` are not
-  const float e2 = big * (1.0f / 8192.0f), mid = unordered(edge);
-  const uint32_t top = ordered(mid + e2), bottom = ordered(mid - e2);
+  const uint32_t top = ordered(unordered(last) + e2);
+  const uint32_t bottom = max(1u, ordered(unordered(first) - e2));
   uint32_t in = 0, between = 0;
-  for (int i = tid; i < cd.n; i += kTopThreads) {
-    const uint32_t u = key(i);
-    in += u > top;
-    between += u <= top && u >= bottom;
+  if (few) {
+#pragma unroll
+    for (int k = 0; k < kTopSteps; ++k) {
+      in += held[k] > top;
+      between += held[k] <= top && held[k] >= bottom;
+    }
+  } else {
+    for (int i = tid; i < cd.n; i += kTopThreads) {
+      const uint32_t u = key(i);
+      in += u > top;
+      between += u <= top && u >= bottom;
+    }
   }
   unsigned long long both = (static_cast<unsigned long long>(in) << 32) | between;
 #pragma unroll
@@ -429,11 +532,15 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     // largest key, the others the smallest
     for (int i = tid; i < cd.n; i += kTopThreads) {
       const uint32_t u = sm.keys[i];
-      if (u <= top && u >= bottom) sm.band[atomicAdd(&sm.band_n, 1u)] = i;
+      if (u <= top && u >= bottom) {
+        const uint32_t at = atomicAdd(&sm.band_n, 1u);
+        sm.band[at] = i;
+        sm.phys[at] = phys_page(a.q, s, a.sink + i);
+      }
     }
     __syncthreads();
     for (uint32_t k = warp; k < between; k += kTopThreads / 32) {
-      const float x = exact_score(a, s, t, g, static_cast<int>(sm.band[k]));
+      const float x = exact_score(a, t, g, sm.phys[k]);
       if (lane == 0) sm.exact[k] = ordered(x);
     }
     __syncthreads();
@@ -456,7 +563,7 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
       while (todo) {
         const int i = base + __ffs(todo) - 1;
         todo &= todo - 1;
-        const float x = exact_score(a, s, t, g, i);
+        const float x = exact_score(a, t, g, phys_page(a.q, s, a.sink + i));
         if (lane == 0) score[i] = make_float2(x, -1.0f);
       }
     }
@@ -467,10 +574,33 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     least = radix_rank(cd.n, exact_key, marked, rank, sm);
     equal = rank;
   }
+  const uint32_t before = (1u << lane) - 1u;
+  if (few && !exact) {
+    // every key from `bottom` on is kept
+    const int i0 = warp * (kTopSteps * 32);
+    uint32_t keep[kTopSteps], at = 0;
+#pragma unroll
+    for (int k = 0; k < kTopSteps; ++k) {
+      const int i = i0 + 32 * k + lane;
+      keep[k] = __ballot_sync(0xffffffffu, i < cd.n && sm.keys[i] >= bottom);
+      at += __popc(keep[k]);
+    }
+    if (lane == 0) sm.red[0][warp] = at;
+    __syncthreads();
+    at = __reduce_add_sync(0xffffffffu, lane < warp ? sm.red[0][lane] : 0u);
+#pragma unroll
+    for (int k = 0; k < kTopSteps; ++k) {
+      const uint32_t pos = at + __popc(keep[k] & before);
+      if (((keep[k] >> lane) & 1u) && pos < static_cast<uint32_t>(a.top))
+        out[head + pos] = a.sink + i0 + 32 * k + lane;
+      at += __popc(keep[k]);
+    }
+    return;
+  }
   // pages above the border, and of those between the ones above `least` with
   // the first `equal` that have it
-  const int per = (cd.n + kTopThreads - 1) / kTopThreads;
-  const int i0 = min(cd.n, tid * per), i1 = min(cd.n, i0 + per);
+  const int per = (cd.n + kTopThreads - 1) / kTopThreads * 32;   // candidates per warp
+  const int i0 = min(cd.n, warp * per), i1 = min(cd.n, i0 + per);
   // 0 dropped, 1 kept, 2 equal to the least
   auto verdict = [&](int i) -> int {
     uint32_t u;
@@ -489,30 +619,29 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     if (i < cap) u = ordered(score[i].x);
     return u > least ? 1 : u == least ? 2 : 0;
   };
-  unsigned long long mine = 0;                      // kept in the high word, equal in the low
-  for (int i = i0; i < i1; ++i) {
-    const int vd = verdict(i);
-    mine += vd == 1 ? 1ull << 32 : static_cast<unsigned long long>(vd >> 1);
+  uint32_t gt = 0, eq = 0;                          // kept, equal to the least
+  for (int base = i0; base < i1; base += 32) {
+    const int vd = base + lane < i1 ? verdict(base + lane) : 0;
+    gt += __popc(__ballot_sync(0xffffffffu, vd == 1));
+    eq += __popc(__ballot_sync(0xffffffffu, vd == 2));
   }
-  unsigned long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+  if (lane == 0) {
+    sm.red[0][warp] = gt;
+    sm.red[1][warp] = eq;
   }
-  if (lane == 31) sm.sums[warp] = incl;
   __syncthreads();
-  unsigned long long excl = incl - mine;
-  for (int w = 0; w < warp; ++w) excl += sm.sums[w];
-  uint32_t gt = static_cast<uint32_t>(excl >> 32), eq = static_cast<uint32_t>(excl);
-  for (int i = i0; i < i1; ++i) {
-    const int vd = verdict(i);
-    const uint32_t at = gt + min(eq, equal);
-    if (vd == 1 || (vd == 2 && eq < equal)) {
-      if (at < static_cast<uint32_t>(a.top)) out[head + at] = a.sink + i;
-    }
-    gt += vd == 1;
-    eq += vd == 2;
+  gt = __reduce_add_sync(0xffffffffu, lane < warp ? sm.red[0][lane] : 0u);
+  eq = __reduce_add_sync(0xffffffffu, lane < warp ? sm.red[1][lane] : 0u);
+  for (int base = i0; base < i1; base += 32) {
+    const int vd = base + lane < i1 ? verdict(base + lane) : 0;
+    const uint32_t keep = __ballot_sync(0xffffffffu, vd == 1);
+    const uint32_t ties = __ballot_sync(0xffffffffu, vd == 2);
+    const uint32_t tie = eq + __popc(ties & before);
+    const uint32_t at = gt + __popc(keep & before) + min(tie, equal);
+    if ((vd == 1 || (vd == 2 && tie < equal)) && at < static_cast<uint32_t>(a.top))
+      out[head + at] = a.sink + base + lane;
+    gt += __popc(keep);
+    eq += __popc(ties);
   }
 }
 
@@ -536,7 +665,9 @@ struct TopWarpSmem {
 };
 
 __global__ void __launch_bounds__(kTopWarpThreads) page_top_warp_kernel(const SelectArgs a) {
-  __shared__ TopWarpSmem smem[kTopWarpThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the attention waits by itself
+  extern __shared__ __align__(16) uint8_t top_smem[];
+  TopWarpSmem* smem = reinterpret_cast<TopWarpSmem*>(top_smem);
   const long long tg =
       static_cast<long long>(blockIdx.x) * (kTopWarpThreads / 32) + (threadIdx.x >> 5);
   if (tg >= static_cast<long long>(a.q.T) * a.Hkv) return;
@@ -546,7 +677,10 @@ __global__ void __launch_bounds__(kTopWarpThreads) page_top_warp_kernel(const Se
   TopWarpSmem& sm = smem[threadIdx.x >> 5];
   int s;
   const Seq q = seq_of_token(a.q, t, s);
-  if (q.n == 0) return;
+  if (q.n == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // not done before the kernel before
+    return;
+  }
   const Candidates cd = candidates(a, q.kv - q.n + (t - q.q0));
   int32_t* out = a.lists + tg * a.width;
   const int kept = min(cd.n, a.top);
@@ -565,8 +699,8 @@ __global__ void __launch_bounds__(kTopWarpThreads) page_top_warp_kernel(const Se
     else if (cd.n <= a.top)
       out[i] = i;
   }
-  if (cd.n <= a.top || a.top == 0) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the scores
+  if (cd.n <= a.top || a.top == 0) return;
   const float2* score = a.score + tg * a.q.per_seq;
   const int steps = (cd.n + 31) >> 5;               // candidate 32 k + lane; key 0: none
   float big = 0.f;
@@ -623,7 +757,7 @@ __global__ void __launch_bounds__(kTopWarpThreads) page_top_warp_kernel(const Se
       while (todo) {
         const int i = 32 * k + __ffs(todo) - 1;
         todo &= todo - 1;
-        const uint32_t x = ordered(exact_score(a, s, t, g, i));
+        const uint32_t x = ordered(exact_score(a, t, g, phys_page(a.q, s, a.sink + i)));
         if (lane == 0) sm.keys[i] = x;
         elo = min(elo, x);
         ehi = max(ehi, x);

@@ -195,6 +195,7 @@ constexpr int kRopeThreads = 256;
 // in halves, has a kernel of its own: 243 us, 5.65 TB/s, against 259.
 template <bool HALVES>
 __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const NormRopeArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long w = (static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x) >> 5;
   if (w >= a.warps) return;
   const int lane = threadIdx.x & 31, li = lane & 7, slot = lane >> 3;

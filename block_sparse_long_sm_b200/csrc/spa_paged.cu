@@ -159,7 +159,8 @@ spa_status paged_checks(const spa_paged_params* p, const spa_rows* q, const int3
 }
 
 // Launch that, with `early`, may begin before the stream's previous kernel has
-// ended; the kernel itself waits for that one's results.
+// ended (2 us less between two kernels); the kernel itself waits for that one
+// before it reads or writes memory.
 template <typename... P, typename... A>
 bool launch_after(bool early, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
                   cudaStream_t stream, const A&... args) {
@@ -175,6 +176,17 @@ bool launch_after(bool early, void (*kernel)(P...), dim3 grid, unsigned threads,
   cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
+
+// Shared memory that spreads `blocks` evenly over the SMs: more than a block's
+// share when one more were to fit.  Blocks that begin as the kernel before
+// leaves the SMs would crowd on the first ones that it leaves (ranking for 16
+// tokens of 8 kv heads, 128 blocks: the whole selecting step 82 us, spread 74).
+size_t spread_smem(long long blocks, size_t own) {
+  const long long per_sm = (blocks + kPagedGrid - 1) / kPagedGrid;
+  const size_t share = (size_t)(233472 / (per_sm + 1)) + 1024;
+  return share > own ? share : own;
+}
+constexpr int kSpreadMax = 233472 / 2 + 1024;
 
 template <bool LIST>
 bool launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -230,11 +242,12 @@ SPA_API spa_status sparse_qk_norm_rope(const spa_rope_params* r, const spa_rows*
   a.err = error_word;
   const long long blocks = (a.warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (blocks > INT_MAX) return SPA_ERR_UNSUPPORTED;
-  if (r->rotary_dim == 128 && !r->interleaved)
-    norm_rope_kernel<true><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(a);
-  else
-    norm_rope_kernel<false><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SPA_OK : SPA_ERR_CUDA;
+  const bool ok = r->rotary_dim == 128 && !r->interleaved
+                      ? launch_after(true, norm_rope_kernel<true>, dim3((unsigned)blocks),
+                                     kRopeThreads, 0, stream, a)
+                      : launch_after(true, norm_rope_kernel<false>, dim3((unsigned)blocks),
+                                     kRopeThreads, 0, stream, a);
+  return ok ? SPA_OK : SPA_ERR_CUDA;
 }
 
 SPA_API spa_status sparse_paged_append(const spa_paged_params* p, const spa_rope_params* r,
@@ -336,15 +349,18 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
     if (cudaGetLastError() != cudaSuccess) return SPA_ERR_CUDA;
   }
   // (begins while the scores are computed: it reads the lengths meanwhile)
-  const unsigned warp_blocks = (unsigned)((tg + kTopWarpThreads / 32 - 1) / (kTopWarpThreads / 32));
   bool ok;
   if (most > kTopWarpKeys) {
-    if (set_smem(page_top_kernel, top_smem_bytes(INT_MAX)) != cudaSuccess) return SPA_ERR_CUDA;
+    static_assert(top_smem_bytes(INT_MAX) <= kSpreadMax, "one limit for both");
+    if (set_smem(page_top_kernel, kSpreadMax) != cudaSuccess) return SPA_ERR_CUDA;
     ok = launch_after(scored, page_top_kernel, dim3((unsigned)tg), kTopThreads,
-                      top_smem_bytes(p->pages_per_seq), stream, a);
+                      spread_smem(tg, top_smem_bytes(p->pages_per_seq)), stream, a);
   } else {
-    ok = launch_after(scored, page_top_warp_kernel, dim3(warp_blocks), kTopWarpThreads, 0, stream,
-                      a);
+    constexpr int warps = kTopWarpThreads / 32;
+    const long long blocks = (tg + warps - 1) / warps;
+    if (set_smem(page_top_warp_kernel, kSpreadMax) != cudaSuccess) return SPA_ERR_CUDA;
+    ok = launch_after(scored, page_top_warp_kernel, dim3((unsigned)blocks), kTopWarpThreads,
+                      spread_smem(blocks, warps * sizeof(TopWarpSmem)), stream, a);
   }
   return ok ? SPA_OK : SPA_ERR_CUDA;
 }

@@ -158,3 +158,23 @@ def test_ties_at_the_border_of_every_size(pages):
     for top in (pages // 7, pages // 2, pages - 3):
         _, _, lists, counts, _ = run_select(b, 1, 1, top, summary=sm)
         check_lists(b, lists, counts, expected(b, sm, 1, 1, top))
+
+
+@pytest.mark.parametrize("pages", [2051, 2052, 5000])
+def test_candidates_around_those_kept_in_registers(pages):
+    b = Batch(4, 1, 16, [(1, 16 * pages - 5)], seed=pages)
+    sm = b.summary()
+    for top in (1, 333, 2047):
+        _, _, lists, counts, _ = run_select(b, 1, 2, top, summary=sm)
+        check_lists(b, lists, counts, expected(b, sm, 1, 2, top))
+    b.ok()
+
+
+def test_more_rankings_than_sms():
+    b = Batch(4, 4, 16, [(12, 16 * 600), (30, 16 * 700 - 9)], seed=8, pad_rows=2)
+    p, sm, lists, counts, ws = run_select(b, 1, 2, 50)
+    want = expected(b, sm, 1, 2, 50)
+    check_lists(b, lists, counts, want)
+    o, lse = attend(b, p, lists, counts, ws=ws)
+    check_attention(b, o, lse, pages_of=lambda t, g: want[(t, g)], rows={0, 11, 12, 41})
+    b.ok()
