@@ -703,34 +703,47 @@ __global__ void __launch_bounds__(kTopWarpThreads) page_top_warp_kernel(const Se
   if (cd.n <= a.top || a.top == 0) return;
   const float2* score = a.score + tg * a.q.per_seq;
   const int steps = (cd.n + 31) >> 5;               // candidate 32 k + lane; key 0: none
+  constexpr int kHeld = kTopWarpKeys / 32;
+  uint32_t held[kHeld];
   float big = 0.f;
   uint32_t lo = 0xffffffffu, hi = 0u;
-#pragma unroll 8
-  for (int k = 0; k < steps; ++k) {
-    const bool on = 32 * k + lane < cd.n;
-    const float2 x = on ? score[32 * k + lane] : make_float2(0.f, 0.f);
-    const uint32_t u = on ? ordered(x.x) : 0u;
-    sm.keys[32 * k + lane] = u;
-    big = fmaxf(big, x.y);
-    lo = on ? min(lo, u) : lo;
-    hi = max(hi, u);
+  {
+    float2 x[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (32 * k + lane < cd.n) x[k] = score[32 * k + lane];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      held[k] = 0u;
+      if (32 * k + lane < cd.n) {
+        held[k] = ordered(x[k].x);
+        big = fmaxf(big, x[k].y);
+        lo = min(lo, held[k]);
+        hi = max(hi, held[k]);
+      }
+      sm.keys[32 * k + lane] = held[k];
+    }
   }
   big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
-  // bits above the highest one in which the keys differ are common to all; every
-  // lane reads only its own keys until the exact ones are written
-  const int bit = 31 - __clz(lo ^ hi);
-  const uint32_t edge =
-      bit_rank(bit >= 31 ? 0u : hi & ~((1u << (bit + 1)) - 1u), bit, a.top, [&](uint32_t c) {
-        uint32_t n = 0;
-#pragma unroll 8
-        for (int k = 0; k < steps; ++k) n += sm.keys[32 * k + lane] >= c;
-        return __reduce_add_sync(0xffffffffu, n);
-      });
+  // The key of rank `top` lies in [first, last], halved until it is no wider than
+  // the error of two sums.
+  const float e2 = big * (1.0f / 8192.0f);
+  uint32_t first = lo, last = hi;
+  while (first < last && !(unordered(last) - unordered(first) <= e2)) {
+    const uint32_t p = first + ((last - first) >> 1) + 1u;
+    uint32_t n = 0;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) n += held[k] >= p;
+    if (__reduce_add_sync(0xffffffffu, n) >= static_cast<uint32_t>(a.top))
+      first = p;
+    else
+      last = p - 1u;
+  }
   // keys above `top` are kept, below `bottom` are not
-  const float e2 = big * (1.0f / 8192.0f), mid = unordered(edge);
-  const uint32_t top = ordered(mid + e2), bottom = max(1u, ordered(mid - e2));
+  const uint32_t top = ordered(unordered(last) + e2);
+  const uint32_t bottom = max(1u, ordered(unordered(first) - e2));
   uint32_t in = 0, between = 0;
 #pragma unroll 4
   for (int k = 0; k < steps; ++k) {
