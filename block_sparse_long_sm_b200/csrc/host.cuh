@@ -196,14 +196,14 @@ bool map_3d(CUtensorMap* m, CUtensorMapDataType dt, size_t esize, const void* ba
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D map over bf16 rows of 128, [outer][inner][128] with the given strides
-// (elements), in boxes of 64 columns x box_inner x box_outer.
+// 3-D map over bf16 rows of `columns`, [outer][inner][columns] with the given
+// strides (elements), in boxes of 64 columns x box_inner x box_outer.
 inline bool map_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                      uint64_t stride_inner, uint64_t stride_outer, uint32_t box_inner,
-                     uint32_t box_outer) {
+                     uint32_t box_outer, uint32_t columns = 128) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {128, inner, outer};
+  const cuuint64_t dims[3] = {columns, inner, outer};
   const cuuint64_t strides[2] = {stride_inner * 2, stride_outer * 2};
   const cuuint32_t box[3] = {64, box_inner, box_outer};
   const cuuint32_t estr[3] = {1, 1, 1};

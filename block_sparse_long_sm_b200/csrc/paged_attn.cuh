@@ -9,7 +9,8 @@
 // Rows.  The q heads of a kv head read the same keys, so a 128-row tile of Q
 // is packed token by token with the group's heads inside: row = token * group
 // + head.  Keys come in tiles of 128, a tile being 128 / page_size whole pages
-// found through the block table, one TMA box per page and 64 columns.
+// found through the block table, one TMA box per page and 64 columns (small
+// pages and few rows: per page).
 //
 // Three ways through a segment, by the rows of its unit:
 //   two row tiles   (more than 128 / group tokens)  A: the first 128 / group
@@ -112,6 +113,13 @@ constexpr int kSegBuf = 16;     // the one in turn
 constexpr int kSegPar = 32;     // << i: parity of buffer i's use
 constexpr int kSegOld = 128;    // << i: it was used before
 constexpr int kFewRows = 16;
+// Pages up to these sizes come as one box of whole rows when rows are few, a key's
+// two 128-byte lines beside one another: a box costs some 50 cycles beside its
+// rows, more than the two-way bank conflicts of reading this layout.  32 tokens
+// of 300 to 16K keys in pages of 16: 185 us instead of 209, but in pages of 32
+// 182.5 instead of 180.5; lists of 1024 keys, which many tokens read from L2, in
+// pages of 32: 159 us instead of 163, of 64: 161 instead of 151.
+constexpr int kWholeRowPages = 16, kWholeRowListPages = 32;
 // Arrivals that free a K, V or Q buffer: of the eight softmax warps and the MMA
 // warp when rows are few, else of the MMA's commit, which counts for all.
 constexpr uint32_t kReaders = 9;
@@ -132,6 +140,7 @@ struct PagedAttnArgs {
   int unit_length;           // length on the line of a full list
   int whole_units;           // lists: CTAs take whole units in turn
   int q_by_rows;             // q's heads lie further apart than its tokens
+  int whole_rows;            // few rows: pages as one box of 256-byte rows
   int Hq, Hkv, group;
   int tpt1;                  // tokens per 128-row tile
   int pitch;                 // 128-element rows between pages
@@ -416,7 +425,7 @@ static_assert(kPagedSegRing + kPagedSegs * sizeof(PagedSeg) <= kPagedMl, "ring")
 // tiles before it, parity: of this segment's exchange, uses1: of accumulator 1
 // before it.  False when a wait gave up.  A function of its own, so that its
 // registers and those of the 128-row softmax are allotted apart.
-template <bool LIST>
+template <bool LIST, bool WHOLE_ROWS>
 __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const FewSeg sg, uint8_t* smem,
                                          uint32_t s_base, uint32_t b0, const WaitCtx wc, int kt,
                                          uint32_t parity, int uses1) {
@@ -427,6 +436,9 @@ __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const FewSeg sg
   const int tb = sg.tb, te = sg.te, keys = sg.keys, g = sg.g, tok0 = sg.tok0, flags = sg.flags;
   const int nrows = sg.ntok * a.group;
   const int r0 = lane >> 2, c2 = 2 * (lane & 3);
+  // a key's two 128-byte lines: 16 KB apart, or beside one another
+  constexpr uint32_t key_bytes = WHOLE_ROWS ? 256u : 128u;
+  constexpr uint32_t half_bytes = WHOLE_ROWS ? 128u : kHalfBytes;
   int seen[2];
   uint32_t qf[8][4];
 #pragma unroll
@@ -461,12 +473,13 @@ __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const FewSeg sg
         for (int e = 0; e < 4; ++e) sc2[n][e] = 0.f;
       // matrix i of a load: key half i / 2 (8 keys each), 16-byte chunk i % 2
       const int key = 16 * warp + ((lane >> 4) << 3) + (lane & 7);
+      const uint32_t kat = s_base + (2u + ks_) * kTileBytes + key * key_bytes;
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
         uint32_t kf[4];
-        const int chunk = (2 * ks + ((lane >> 3) & 1)) & 7;
-        ldsm4(kf, (s_base + (2u + ks_) * kTileBytes) + (ks >> 2) * kHalfBytes + key * 128u +
-                      ((chunk ^ (key & 7)) << 4));
+        const uint32_t line = kat + (ks >> 2) * half_bytes;    // its chunks are permuted by its address
+        const uint32_t chunk = (2 * ks + ((lane >> 3) & 1)) & 7;
+        ldsm4(kf, line + ((chunk << 4) ^ ((line >> 3) & 0x70u)));
         mma_16816(sc2[0], qf[ks], kf[0], kf[1]);
         mma_16816(sc2[1], qf[ks], kf[2], kf[3]);
       }
@@ -517,12 +530,13 @@ __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const FewSeg sg
     if (left > 0) {
       // matrix i: key half i % 2, 16-byte chunk i / 2 of a pair
       const int key = 16 * warp + (lane & 15);
+      const uint32_t vat = s_base + (2u + kPagedKStages + vs_) * kTileBytes + key * key_bytes;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint32_t vf[4];
-        const int chunk = (2 * j + (lane >> 4)) & 7;
-        ldsm4_t(vf, (s_base + (2u + kPagedKStages + vs_) * kTileBytes) + (j >> 2) * kHalfBytes + key * 128u +
-                        ((chunk ^ (key & 7)) << 4));
+        const uint32_t line = vat + (j >> 2) * half_bytes;
+        const uint32_t chunk = (2 * j + (lane >> 4)) & 7;
+        ldsm4_t(vf, line + ((chunk << 4) ^ ((line >> 3) & 0x70u)));
         if (left < 16) {
           // rows behind the last key: their probability is 0, but 0 * NaN is not
 #pragma unroll
@@ -614,6 +628,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_k2,   // whole rows
+                  const __grid_constant__ CUtensorMap tm_v2,
                   const __grid_constant__ PagedAttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -665,6 +681,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
+    if (a.whole_rows) {
+      prefetch_tensormap(&tm_k2);
+      prefetch_tensormap(&tm_v2);
+    }
   }
   if (warp == 9) {
     tmem_alloc(smem_u32(tmem_holder), 512);
@@ -748,6 +768,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
       for (int i = 0; ok && take(i, sg, &mine); ++i) {
         if (sg.keys == 0) continue;
         const bool duo = (sg.flags & kSegDuo) != 0, few = (sg.flags & kSegFew) != 0;
+        const bool rows256 = few && a.whole_rows;
         for (int buf = 0; buf < 2; ++buf) {
           if (!duo && !few && buf != ((sg.flags & kSegBuf) ? 1 : 0)) continue;
           const int par = (sg.flags & (kSegPar << buf)) ? 1 : 0;
@@ -803,9 +824,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           if (lane == 0) mbar_arrive_expect_tx(bars.kfull(ks), live * 2u * page_half);
           __syncwarp();
           if (phys >= 0) {
-            const uint32_t at = s_k(ks) + lane * page_half;
-            tma_load_2d(at, &tm_k, bars.kfull(ks), 0, row);
-            tma_load_2d(at + kHalfBytes, &tm_k, bars.kfull(ks), 64, row);
+            if (rows256) {
+              tma_load_3d(s_k(ks) + 2u * lane * page_half, &tm_k2, bars.kfull(ks), 0, 0, row);
+            } else {
+              const uint32_t at = s_k(ks) + lane * page_half;
+              tma_load_2d(at, &tm_k, bars.kfull(ks), 0, row);
+              tma_load_2d(at + kHalfBytes, &tm_k, bars.kfull(ks), 64, row);
+            }
           }
           __syncwarp();
           if (vu > 0 && !(ok = warp_wait(bars.vempty(vs), (vu - 1) & 1, wc))) {
@@ -816,9 +841,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
           if (lane == 0) mbar_arrive_expect_tx(bars.vfull(vs), live * 2u * page_half);
           __syncwarp();
           if (phys >= 0) {
-            const uint32_t at = s_v(vs) + lane * page_half;
-            tma_load_2d(at, &tm_v, bars.vfull(vs), 0, row);
-            tma_load_2d(at + kHalfBytes, &tm_v, bars.vfull(vs), 64, row);
+            if (rows256) {
+              tma_load_3d(s_v(vs) + 2u * lane * page_half, &tm_v2, bars.vfull(vs), 0, 0, row);
+            } else {
+              const uint32_t at = s_v(vs) + lane * page_half;
+              tma_load_2d(at, &tm_v, bars.vfull(vs), 0, row);
+              tma_load_2d(at + kHalfBytes, &tm_v, bars.vfull(vs), 64, row);
+            }
           }
           __syncwarp();
         }
@@ -1061,7 +1090,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         const FewSeg own{sg.tb, te, flags, sg.keys, sg.tok0, sg.ntok, sg.pos0, sg.g};
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.wempty(i % kPagedSegs));
-        if (!(ok = few_segment<LIST>(a, own, smem, s_base, b0, wc, kt, fc++ & 1, oc[1]))) break;
+        ok = a.whole_rows
+                 ? few_segment<LIST, true>(a, own, smem, s_base, b0, wc, kt, fc & 1, oc[1])
+                 : few_segment<LIST, false>(a, own, smem, s_base, b0, wc, kt, fc & 1, oc[1]);
+        if (!ok) break;
+        ++fc;
         kt += te - own.tb;
         continue;
       }

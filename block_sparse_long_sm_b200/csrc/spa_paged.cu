@@ -190,10 +190,11 @@ constexpr int kSpreadMax = 233472 / 2 + 1024;
 
 template <bool LIST>
 bool launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                  const PagedAttnArgs& a, int combine_y, cudaStream_t stream) {
+                  const CUtensorMap& tk2, const CUtensorMap& tv2, const PagedAttnArgs& a,
+                  int combine_y, cudaStream_t stream) {
   if (set_smem(paged_attn_kernel<LIST>, kPagedSmemBytes) != cudaSuccess) return false;
   if (!launch_after(true, paged_attn_kernel<LIST>, dim3(kPagedGrid), kPagedThreads, kPagedSmemBytes,
-                    stream, tq, tk, tv, a))
+                    stream, tq, tk, tv, tk2, tv2, a))
     return false;
   if (a.whole_units) return true;
   return launch_after(true, paged_combine_kernel, dim3(kPagedGrid, combine_y), kCombineThreads, 0,
@@ -421,7 +422,7 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
   a.debug = p->debug_flags;
   const uint64_t cache_rows =
       (uint64_t)a.pitch * (p->num_pages - 1) + (uint64_t)p->heads_kv * p->page_size;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, tk2 = {}, tv2 = {};
   const bool q_map =
       by_rows ? map_rows(&tq, q->data, p->tokens, p->heads_q, st_q, sh, 1, 1)
               : map_rows(&tq, q->data, p->heads_q, p->tokens, sh, st_q, group, a.tpt1);
@@ -429,13 +430,18 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
       !map_2d(&tk, kBF16, 2, k_cache, 128, cache_rows, 64, p->page_size, kSW128) ||
       !map_2d(&tv, kBF16, 2, v_cache, 128, cache_rows, 64, p->page_size, kSW128))
     return SPA_ERR_CUDA;
+  a.whole_rows = p->page_size <= (lists ? kWholeRowListPages : kWholeRowPages);
+  if (a.whole_rows &&
+      (!map_rows(&tk2, k_cache, 2, cache_rows, 64, 128, 2, p->page_size, 64) ||
+       !map_rows(&tv2, v_cache, 2, cache_rows, 64, 128, 2, p->page_size, 64)))
+    return SPA_ERR_CUDA;
   // combine blocks beside one another: a warp per row of a usual unit (four
   // rows by a quarter of the columns)
   long long rows = lists ? group : (long long)p->tokens * group / p->seqs;
   if (rows > kPagedSlotRows) rows = kPagedSlotRows;
   const int cy = rows > 16 ? (int)(rows + 15) / 16 : 1;
-  const bool ok = lists ? launch_paged<true>(tq, tk, tv, a, cy, stream)
-                        : launch_paged<false>(tq, tk, tv, a, cy, stream);
+  const bool ok = lists ? launch_paged<true>(tq, tk, tv, tk2, tv2, a, cy, stream)
+                        : launch_paged<false>(tq, tk, tv, tk2, tv2, a, cy, stream);
   return ok ? SPA_OK : SPA_ERR_CUDA;
 }
 
