@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional
 
 try:                        # device memory and streams; raw addresses need neither
@@ -131,7 +132,7 @@ def _load():
     lib.sparse_key_mass.argtypes = [P, vp, vp, vp, i32, vp, sz, vp, vp]
     lib.sparse_key_mass.restype = ctypes.c_int
     R, G = ctypes.POINTER(SpaRopeParams), ctypes.POINTER(SpaPagedParams)
-    rows = ctypes.POINTER(SpaRows)
+    rows = vp                        # a reference to an SpaRows, or the bytes of one
     lib.sparse_qk_norm_rope.argtypes = [R, rows, rows, vp, vp, vp, vp, rows, rows, vp, vp]
     lib.sparse_qk_norm_rope.restype = ctypes.c_int
     lib.sparse_paged_append.argtypes = [G, R, rows, rows, rows, vp, vp, vp, vp, vp, vp, rows, vp,
@@ -319,9 +320,14 @@ def make_paged_params(heads_q: int, heads_kv: int, *, page_size: int, num_pages:
                           top_pages, int(wait_limit_us), int(debug_flags))
 
 
+_pack_rows = struct.Struct("@Pqqq").pack
+assert struct.calcsize("@Pqqq") == ctypes.sizeof(SpaRows)
+
+
 def _rows(x, batch, tokens, heads, name):
     """A bf16 tensor [batch, tokens, heads, 128] or, for one batch element, [tokens, heads, 128]
-    (any strides but the last dimension's), or an SpaRows, as a reference to spa_rows."""
+    (any strides but the last dimension's), or an SpaRows, as a spa_rows to point at (its bytes:
+    packing them takes a third of the time of making an SpaRows)."""
     if x is None:
         return None
     if x.__class__ is SpaRows:
@@ -341,7 +347,7 @@ def _rows(x, batch, tokens, heads, name):
         raise TypeError(f"{name}: {x.dtype}, wanted torch.bfloat16")
     if s_d != 1 and x.numel():
         raise ValueError(f"{name}: the 128 elements of a row have to be contiguous")
-    return ctypes.byref(SpaRows(x.data_ptr(), sb, s_t, s_h))
+    return _pack_rows(x.data_ptr(), sb, s_t, s_h)
 
 
 def _flat(x, dtype, count, name):

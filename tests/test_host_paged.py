@@ -145,10 +145,10 @@ def test_empty_calls_launch_nothing():
 
 def test_tensor_checks_of_the_binding():
     x = torch.zeros(4, 4, 128, dtype=torch.bfloat16)
-    rows = binding._rows(x, 1, 4, 4, "q")._obj
+    rows = binding.SpaRows.from_buffer_copy(binding._rows(x, 1, 4, 4, "q"))
     assert (rows.stride_batch, rows.stride_token, rows.stride_head) == (0, 512, 128)
     y = torch.zeros(2, 3, 5, 128, dtype=torch.bfloat16).transpose(1, 2)
-    rows = binding._rows(y, 2, 5, 3, "q")._obj
+    rows = binding.SpaRows.from_buffer_copy(binding._rows(y, 2, 5, 3, "q"))
     assert (rows.stride_batch, rows.stride_token, rows.stride_head) == (1920, 128, 640)
     for bad, exc in ((x.half(), TypeError), (x[:3], ValueError),
                      (x.transpose(1, 2).contiguous().transpose(1, 2), ValueError)):
