@@ -37,17 +37,18 @@
 //                    sixteen rows share the loads.  16 sequences of up to 32K in
 //                    pages of 16: 50 MB of summaries, 22 us (2.3 TB/s); 250 tokens
 //                    that share 6 MB: 32 us (loads from L2, three products a page).
-// page_top_kernel    one block per token and kv head: radix search of the
-//                    score of rank top_pages, the exact sums between, and one
-//                    scan that writes the kept pages in ascending order.  Bound
-//                    by latency, a dozen barriers and the loads between: 14 us for
-//                    one token among 2042 pages, 21 us for 16 tokens.
-// page_top_warp_kernel  the same by one warp, for up to 512 candidates: the score
-//                    of rank top_pages is found bit by bit, a count over the
-//                    warp each.  No barriers, and all of a chunk's tokens are
-//                    under way at once: 25 us instead of 37 for 2000 selections
-//                    among 506 pages.  (Among 2048 pages a warp takes 50 us, a
-//                    block 14.)
+// page_top_kernel    one block per token and kv head: the score of rank top_pages
+//                    is found to within the error of the sums, by counting keys
+//                    above three points of an interval (up to 2048 candidates,
+//                    keys in registers) or by a radix search; then the exact sums
+//                    between, and one scan that writes the kept pages in ascending
+//                    order.  Bound by latency, the barriers and the loads between:
+//                    8.4 us for one token among 2042 pages, 9.9 us for 16 (with a
+//                    radix search there: 14 and 17 us).
+// page_top_warp_kernel  the same by one warp, for up to 512 candidates: no barriers,
+//                    and all of a chunk's tokens are under way at once: 20 us for
+//                    2000 selections among 506 pages, the whole step 211 us (218 us
+//                    with a block each).
 #pragma once
 
 #include "paged_seqs.cuh"
