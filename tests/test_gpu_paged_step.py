@@ -307,3 +307,57 @@ def test_lists_out_of_order_or_out_of_sight_are_reported(entries, count):
     counts = torch.tensor([count, 3], dtype=torch.int32, device="cuda").view(1, 2)
     attend(b, p, lists, counts)
     assert spa.sparse_paged_status(b.error) == spa.SPA_ERR_INVALID
+
+
+def test_captured_behind_copies_and_joined_streams():
+    """Calls whose predecessors in a graph are copies, fills and kernels of two streams; each
+    reads what those have just written."""
+    b = Batch(8, 2, 16, [(1, 300), (4, 900), (1, 40)], seed=21)
+    p = b.params(sink_pages=1, local_pages=2, top_pages=5)
+    ws, sm = b.workspace(p), to_gpu(b.summary())
+    r = spa.make_rope_params(1, b.T, 8, 2, table_rows=1024)
+    table = torch.from_numpy(op.rope_table(1024, D)).cuda()
+    pos = torch.tensor([pos for _, _, pos in b.tokens()], dtype=torch.int32, device="cuda")
+    source, staged, turned = b.q.clone(), torch.zeros_like(b.q), torch.zeros_like(b.q)
+    lens, kv = b.kv_gpu.clone(), torch.zeros_like(b.kv_gpu)
+    lists = torch.zeros(b.T, 2, 8, dtype=torch.int32, device="cuda")
+    counts = torch.zeros(b.T, 2, dtype=torch.int32, device="cuda")
+    outs = [torch.zeros(b.T, 8, D, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    lses = [torch.zeros(b.T, 8, device="cuda") for _ in range(2)]
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            kv.copy_(lens)
+        staged.copy_(source)
+        spa.check(spa.sparse_qk_norm_rope(r, staged, None, None, None, pos, table, turned, None,
+                                          b.error))
+        here.wait_stream(side)                                # a copy and a kernel before it
+        spa.check(spa.sparse_paged_attn(p, turned, b.kc, b.vc, b.cu_gpu, kv, b.table_gpu, None, None,
+                                        outs[0], lses[0], ws, b.error))
+        lists.zero_()
+        spa.check(spa.sparse_paged_select(p, turned, sm, b.cu_gpu, kv, b.table_gpu, lists, counts,
+                                          ws, b.error))
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            outs[1].fill_(3.0)
+        here.wait_stream(side)                                # two kernels before it
+        spa.check(spa.sparse_paged_attn(p, turned, b.kc, b.vc, b.cu_gpu, kv, b.table_gpu, lists,
+                                        counts, outs[1], lses[1], ws, b.error))
+    step()
+    torch.cuda.synchronize()
+    tensors = [turned, lists, counts, *outs, *lses]
+    want = [x.clone() for x in tensors]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for x in tensors + [staged, kv]:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(tensors, want):
+            assert torch.equal(x, y)
+    b.ok()
