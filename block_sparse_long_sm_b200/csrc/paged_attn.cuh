@@ -393,6 +393,14 @@ __device__ __forceinline__ int few_at(int row, int col) {
   return row * 128 + (col ^ ((row & 7) << 3));
 }
 
+// Index of a warp's (m, l) of a row when rows are few.  Warps of warpgroup 0 may
+// still read the second accumulator's statistics of the segment before, warp w
+// those of rows 32 w .. 32 w + 31, and nothing orders them against one another:
+// each overwrites only entries that it alone reads.  Warpgroup 1 waits for them.
+__device__ constexpr int few_ml(int warp, int row) {
+  return (warp & 3) * 32 + (warp >> 2) * 16 + row;
+}
+
 // Barriers, 8 bytes each from b0.
 struct PagedBars {
   uint32_t b0;
@@ -555,7 +563,7 @@ __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const FewSeg sg
   // join the eight warps: the Q buffers are the exchange area
   for (int b = 0; b < 2; ++b)
     if (!warp_wait(bars.qfull(b), (flags & (kSegPar << b)) ? 1 : 0, wc)) return false;
-  // (warpgroup 0 may still read ml for an earlier segment's second accumulator)
+  // (warpgroup 0 may still read ml for an earlier segment's second accumulator, see few_ml)
   if (warp >= 4 && uses1 > 0 && !warp_wait(bars.ofree(1), (uses1 - 1) & 1, wc)) return false;
   float* area = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -569,8 +577,8 @@ __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const FewSeg sg
         *reinterpret_cast<float2*>(area + warp * 2048 + few_at(rr, 8 * j + c2)) =
             make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
       if ((lane & 3) == 0) {
-        ml[warp * 16 + rr] = m[e];
-        ml[128 + warp * 16 + rr] = l[e];
+        ml[few_ml(warp, rr)] = m[e];
+        ml[128 + few_ml(warp, rr)] = l[e];
       }
     }
   }
@@ -582,13 +590,13 @@ __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const FewSeg sg
   for (int rr = warp; rr < nrows; rr += 8) {
     float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) mm = fmaxf(mm, ml[w * 16 + rr]);
+    for (int w = 0; w < 8; ++w) mm = fmaxf(mm, ml[few_ml(w, rr)]);
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-      const float mw = ml[w * 16 + rr];
+      const float mw = ml[few_ml(w, rr)];
       const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - mm);
-      ll = fmaf(ml[128 + w * 16 + rr], f, ll);
+      ll = fmaf(ml[128 + few_ml(w, rr)], f, ll);
       const float4 x = *reinterpret_cast<const float4*>(area + w * 2048 + few_at(rr, 4 * lane));
       y.x = fmaf(x.x, f, y.x);
       y.y = fmaf(x.y, f, y.y);
