@@ -623,6 +623,8 @@ __device__ __noinline__ bool few_segment(const PagedAttnArgs& a, const FewSeg sg
       }
     }
   }
+  // the next contents of the area may come by a copy (async proxy)
+  fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
     mbar_arrive(bars.qfree(0));
