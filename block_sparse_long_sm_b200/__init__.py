@@ -18,8 +18,9 @@ _BINDING_NAMES = (
     "kept_flops", "make_paged_params", "make_params", "make_rope_params",
     "sparse_decode_attn", "sparse_decode_prepare", "sparse_decode_scratch_bytes",
     "sparse_fp8_quantize", "sparse_fp8_scales_floats", "sparse_fp8_scratch_bytes",
-    "sparse_key_mass", "sparse_paged_append", "sparse_paged_attn", "sparse_paged_select",
-    "sparse_paged_status", "sparse_paged_workspace_bytes", "sparse_prefill_attn", "sparse_prefill_attn_fp8", "sparse_prefill_plan",
+    "sparse_key_mass", "sparse_paged_append", "sparse_paged_attn",
+    "sparse_paged_attn_workspace_bytes", "sparse_paged_select", "sparse_paged_status",
+    "sparse_paged_workspace_bytes", "sparse_prefill_attn", "sparse_prefill_attn_fp8", "sparse_prefill_plan",
     "sparse_prefill_plan_static", "sparse_prefill_stats", "sparse_prefill_status_string",
     "sparse_prefill_workspace_bytes", "sparse_qk_norm_rope")
 

@@ -34,8 +34,9 @@ EXPORTED = ("sparse_prefill_workspace_bytes", "sparse_prefill_plan", "sparse_pre
             "sparse_decode_scratch_bytes", "sparse_decode_prepare", "sparse_decode_attn",
             "sparse_fp8_scales_floats", "sparse_fp8_scratch_bytes", "sparse_fp8_quantize",
             "sparse_prefill_attn_fp8", "sparse_key_mass", "sparse_qk_norm_rope",
-            "sparse_paged_append", "sparse_paged_workspace_bytes", "sparse_paged_select",
-            "sparse_paged_attn", "sparse_paged_status")
+            "sparse_paged_append", "sparse_paged_workspace_bytes",
+            "sparse_paged_attn_workspace_bytes", "sparse_paged_select", "sparse_paged_attn",
+            "sparse_paged_status")
 
 
 class SpaParams(ctypes.Structure):
@@ -140,6 +141,8 @@ def _load():
     lib.sparse_paged_append.restype = ctypes.c_int
     lib.sparse_paged_workspace_bytes.argtypes = [G]
     lib.sparse_paged_workspace_bytes.restype = sz
+    lib.sparse_paged_attn_workspace_bytes.argtypes = [G]
+    lib.sparse_paged_attn_workspace_bytes.restype = sz
     lib.sparse_paged_select.argtypes = [G, rows, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
     lib.sparse_paged_select.restype = ctypes.c_int
     lib.sparse_paged_attn.argtypes = [G, rows, vp, vp, vp, vp, vp, vp, vp, rows, vp, vp, sz, vp,
@@ -461,7 +464,13 @@ def sparse_paged_append(params: SpaPagedParams, rope: Optional[SpaRopeParams], q
 
 
 def sparse_paged_workspace_bytes(params: SpaPagedParams) -> int:
+    """Workspace that serves the selection and the attention."""
     return int(_lib.sparse_paged_workspace_bytes(ctypes.byref(params)))
+
+
+def sparse_paged_attn_workspace_bytes(params: SpaPagedParams) -> int:
+    """Workspace of the attention alone, the same for every batch."""
+    return int(_lib.sparse_paged_attn_workspace_bytes(ctypes.byref(params)))
 
 
 def _list_width(p: SpaPagedParams) -> int:

@@ -129,7 +129,8 @@ struct PagedLayout {
 };
 
 // Workspace (byte offsets, each region 256-aligned): unit records, partial
-// results of the attention (two slots of 256 rows per CTA), page scores.
+// results of the attention (two slots of 256 rows per CTA), page scores.  The
+// attention uses what lies before the scores.
 PagedLayout paged_layout(const spa_paged_params* p) {
   PagedLayout lo;
   size_t off = 0;
@@ -147,15 +148,22 @@ PagedLayout paged_layout(const spa_paged_params* p) {
 
 spa_status paged_checks(const spa_paged_params* p, const spa_rows* q, const int32_t* cu_q,
                         const int32_t* kv_lens, const int32_t* table, const void* workspace,
-                        size_t bytes, const uint32_t* err) {
+                        size_t bytes, const uint32_t* err, bool scores) {
   spa_status st = validate_paged(p);
   if (st != SPA_OK) return st;
   if (!workspace || !aligned16(workspace) || !word_ok(err)) return SPA_ERR_INVALID;
-  if (bytes < paged_layout(p).total) return SPA_ERR_WORKSPACE;
+  const PagedLayout lo = paged_layout(p);
+  if (bytes < (scores ? lo.total : lo.score)) return SPA_ERR_WORKSPACE;
   if (p->tokens == 0 || p->seqs == 0) return SPA_OK;
   if (!rows_ok(q) || !word_ok(cu_q) || !word_ok(kv_lens) || !word_ok(table))
     return SPA_ERR_INVALID;
   return SPA_OK;
+}
+
+// Whether a token can have more candidate pages than the selection keeps.
+bool ranks(const spa_paged_params* p) {
+  return p->top_pages > 0 &&
+         (long long)p->pages_per_seq - p->sink_pages - p->local_pages > p->top_pages;
 }
 
 // Launch that, with `early`, may begin before the stream's previous kernel has
@@ -310,6 +318,11 @@ SPA_API size_t sparse_paged_workspace_bytes(const spa_paged_params* p) {
   return paged_layout(p).total;
 }
 
+SPA_API size_t sparse_paged_attn_workspace_bytes(const spa_paged_params* p) {
+  if (validate_paged(p) != SPA_OK) return 0;
+  return paged_layout(p).score;
+}
+
 SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows* q,
                                        const void* summary, const int32_t* cu_q,
                                        const int32_t* kv_lens, const int32_t* block_table,
@@ -317,7 +330,7 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
                                        size_t workspace_bytes, uint32_t* error_word,
                                        cudaStream_t stream) {
   spa_status st = paged_checks(p, q, cu_q, kv_lens, block_table, workspace, workspace_bytes,
-                               error_word);
+                               error_word, p && ranks(p));
   if (st != SPA_OK) return st;
   if (p->tokens == 0 || p->seqs == 0) return SPA_OK;
   if (!summary || !aligned16(summary) || !word_ok(lists) || !word_ok(counts))
@@ -340,7 +353,7 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
   const long long most = (long long)p->pages_per_seq - a.sink - a.local;   // candidates
   const long long tg = (long long)p->tokens * p->heads_kv;
   if (tg > INT_MAX) return SPA_ERR_UNSUPPORTED;
-  const bool scored = most > a.top && a.top > 0;
+  const bool scored = ranks(p);
   if (scored) {
     const long long groups = ((long long)p->tokens + a.tm - 1) / a.tm * p->heads_kv;
     a.chunks = (int)((most + kScorePages - 1) / kScorePages);
@@ -374,7 +387,7 @@ SPA_API spa_status sparse_paged_attn(const spa_paged_params* p, const spa_rows* 
                                      void* workspace, size_t workspace_bytes,
                                      uint32_t* error_word, cudaStream_t stream) {
   spa_status st = paged_checks(p, q, cu_q, kv_lens, block_table, workspace, workspace_bytes,
-                               error_word);
+                               error_word, false);
   if (st != SPA_OK) return st;
   if ((lists == nullptr) != (counts == nullptr)) return SPA_ERR_INVALID;
   if (p->tokens == 0 || p->seqs == 0) return SPA_OK;

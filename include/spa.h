@@ -432,9 +432,16 @@ SPA_API spa_status sparse_paged_append(const spa_paged_params* p, const spa_rope
                                        const spa_rows* q_out, void* k_cache, void* v_cache,
                                        void* summary, uint32_t* error_word, cudaStream_t stream);
 
-/* Device workspace of sparse_paged_select and sparse_paged_attn (closed form;
- * 0 when the params are invalid).  Needs no initialisation. */
+/* Device workspace that serves sparse_paged_select and sparse_paged_attn (closed
+ * form; 0 when the params are invalid).  Needs no initialisation.  Beside the
+ * attention's part it holds eight bytes of scores per token, kv head and entry
+ * of pages_per_seq. */
 SPA_API size_t sparse_paged_workspace_bytes(const spa_paged_params* p);
+
+/* What sparse_paged_attn alone needs, with lists or without: its part of the
+ * above, 39 MB whatever the batch.  It also does for sparse_paged_select where
+ * nothing is ranked (top_pages = 0, or no more candidates than that). */
+SPA_API size_t sparse_paged_attn_workspace_bytes(const spa_paged_params* p);
 
 /* Pages of every new token t and kv head g.  With x the token's position, its
  * visible pages are 0 .. x / page_size.  Kept are the first sink_pages, the

@@ -138,3 +138,16 @@ def test_batches_that_mix_tokens_and_chunks(hq, hkv, page, seed):
     rows = set(int(t) for t in np.random.default_rng(seed).permutation(b.T)[:60])
     check_attention(b, o, lse, rows=rows | set(int(x) for x in b.cu[:-1]))
     b.ok()
+
+
+@pytest.mark.parametrize("seqs", [[(1, 3000), (1, 77)], [(300, 2000), (1, 40)]])
+def test_attention_stays_within_its_own_workspace(seqs):
+    b = Batch(8, 2, 16, seqs, seed=12)
+    p = b.params()
+    n = spa.sparse_paged_attn_workspace_bytes(p)
+    assert n < spa.sparse_paged_workspace_bytes(p)
+    ws = torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    o, lse = attend(b, p, ws=ws[:n])
+    check_attention(b, o, lse, rows={0, 1, 127, 128, 299, 300})
+    assert bool((ws[n:] == 0xFF).all())
+    b.ok()

@@ -66,6 +66,31 @@ def test_workspace_is_closed_form_and_covers_its_parts():
     assert m - n >= (1000 * 4096 - 4 * 4) * 2 * 4 - 256
 
 
+def test_plain_attention_needs_no_room_for_scores():
+    # a 16K chunk over 128K positions in pages of 16: the scores alone would be 1 GB per kv head
+    small, large = paged(), paged(tokens=16384, pages_per_seq=8192)
+    ranked = paged(tokens=16384, pages_per_seq=8192, top_pages=8)
+    base = spa.sparse_paged_attn_workspace_bytes(small)
+    assert base == spa.sparse_paged_attn_workspace_bytes(large)
+    assert base == spa.sparse_paged_attn_workspace_bytes(ranked)
+    assert 2 * 148 * 256 * 130 * 4 <= base < 40 << 20
+    assert base <= spa.sparse_paged_workspace_bytes(small)
+    assert spa.sparse_paged_attn_workspace_bytes(paged(head_dim=64)) == 0
+    odd = spa.SpaRows(A, 0, 384, 256)      # refused behind the workspace's check
+    for lists in (None, A):
+        for p in (large, ranked):
+            kw = dict(q=odd, lists=lists, counts=lists)
+            assert attn(p, nbytes=base, **kw) == spa.SPA_ERR_UNSUPPORTED
+            assert attn(p, nbytes=base - 1, **kw) == spa.SPA_ERR_WORKSPACE
+    # the selection wants its scores' room when it ranks
+    full = spa.sparse_paged_workspace_bytes(ranked)
+    assert full - base >= 16384 * 2 * 8191 * 8
+    assert select(ranked, nbytes=full, summary=0) == spa.SPA_ERR_INVALID
+    assert select(ranked, nbytes=full - 1, summary=0) == spa.SPA_ERR_WORKSPACE
+    assert select(large, nbytes=base, summary=0) == spa.SPA_ERR_INVALID
+    assert select(large, nbytes=base - 1, summary=0) == spa.SPA_ERR_WORKSPACE
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(ws=0), spa.SPA_ERR_INVALID), (dict(ws=A + 8), spa.SPA_ERR_INVALID),
     (dict(nbytes=100), spa.SPA_ERR_WORKSPACE), (dict(err=0), spa.SPA_ERR_INVALID),
