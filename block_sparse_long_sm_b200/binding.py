@@ -366,8 +366,37 @@ def _flat(x, dtype, count, name):
     return x.data_ptr()
 
 
+def _grid(x, dtype, shape, name):
+    """Address of a contiguous tensor that the library reads as [shape]: of that shape, with more
+    rows in front, or flat.  Rows of another length would be read with the wrong stride."""
+    if x is None or x.__class__ is int:
+        return x
+    if x.shape == shape and x.dtype is dtype and x.is_contiguous():
+        return x.data_ptr()
+    dim, count = x.dim(), math.prod(shape)
+    if dim == len(shape):
+        # a dimension's length is a stride unless there is only one row of it
+        rows, good = 1, True
+        for have, want in zip(x.shape, shape):
+            good = good and (have == want or (have > want and rows <= 1))
+            rows *= want
+    else:
+        good = dim == 1 or x.numel() == count
+    if not good:
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted {shape}")
+    return _flat(x, dtype, count, name)
+
+
 _I32, _BF16, _F32, _U32 = (getattr(_torch, t, None)
                            for t in ("int32", "bfloat16", "float32", "uint32"))
+_WEIGHT = (128,)
+
+
+def _angles(r, table):
+    """Address of the rotation table; unused, and so unchecked, without a rotation."""
+    if r is None or r.rotary_dim == 0:
+        return _flat(table, _F32, 0, "table")
+    return _grid(table, _F32, (r.table_rows, r.rotary_dim), "table")
 
 
 def _word(x):
@@ -437,9 +466,9 @@ def sparse_qk_norm_rope(params: SpaRopeParams, q, k, q_weight, k_weight, positio
     dev = _device(q, k, q_weight, k_weight, positions, table, q_out, k_out, error)
     return _call(
         _lib.sparse_qk_norm_rope, dev, stream, ctypes.byref(r), _rows(q, b, t, hq, "q"),
-        _rows(k, b, t, hk, "k"), _flat(q_weight, _BF16, 128, "q_weight"),
-        _flat(k_weight, _BF16, 128, "k_weight"), _flat(positions, _I32, b * t, "positions"),
-        _flat(table, _F32, r.table_rows * r.rotary_dim, "table"), _rows(q_out, b, t, hq, "q_out"),
+        _rows(k, b, t, hk, "k"), _grid(q_weight, _BF16, _WEIGHT, "q_weight"),
+        _grid(k_weight, _BF16, _WEIGHT, "k_weight"), _grid(positions, _I32, (b, t), "positions"),
+        _angles(r, table), _rows(q_out, b, t, hq, "q_out"),
         _rows(k_out, b, t, hk, "k_out"), _word(error))
 
 
@@ -454,13 +483,14 @@ def sparse_paged_append(params: SpaPagedParams, rope: Optional[SpaRopeParams], q
     return _call(
         _lib.sparse_paged_append, dev, stream, ctypes.byref(p),
         None if rope is None else ctypes.byref(rope), _rows(q, 1, t, hq, "q"),
-        _rows(k, 1, t, hk, "k"), _rows(v, 1, t, hk, "v"), _flat(q_weight, _BF16, 128, "q_weight"),
-        _flat(k_weight, _BF16, 128, "k_weight"),
-        _flat(table, _F32, 0 if rope is None else rope.table_rows * rope.rotary_dim, "table"),
-        _flat(cu_q, _I32, seqs + 1, "cu_q"), _flat(kv_lens, _I32, seqs, "kv_lens"),
-        _flat(block_table, _I32, seqs * p.pages_per_seq, "block_table"), _rows(q_out, 1, t, hq, "q_out"),
+        _rows(k, 1, t, hk, "k"), _rows(v, 1, t, hk, "v"),
+        _grid(q_weight, _BF16, _WEIGHT, "q_weight"), _grid(k_weight, _BF16, _WEIGHT, "k_weight"),
+        _angles(rope, table), _flat(cu_q, _I32, seqs + 1, "cu_q"),
+        _flat(kv_lens, _I32, seqs, "kv_lens"),
+        _grid(block_table, _I32, (seqs, p.pages_per_seq), "block_table"),
+        _rows(q_out, 1, t, hq, "q_out"),
         _cache(p, k_cache, "k_cache"), _cache(p, v_cache, "v_cache"),
-        _flat(summary, _BF16, p.num_pages * hk * 256, "summary"), _word(error))
+        _grid(summary, _BF16, (p.num_pages, hk, 2, 128), "summary"), _word(error))
 
 
 def sparse_paged_workspace_bytes(params: SpaPagedParams) -> int:
@@ -486,10 +516,11 @@ def sparse_paged_select(params: SpaPagedParams, q, summary, cu_q, kv_lens, block
     wb = _nbytes(workspace) if workspace_bytes is None else int(workspace_bytes)
     return _call(
         _lib.sparse_paged_select, dev, stream, ctypes.byref(p), _rows(q, 1, t, p.heads_q, "q"),
-        _flat(summary, _BF16, p.num_pages * hk * 256, "summary"), _flat(cu_q, _I32, seqs + 1, "cu_q"),
-        _flat(kv_lens, _I32, seqs, "kv_lens"), _flat(block_table, _I32, seqs * p.pages_per_seq, "block_table"),
-        _flat(lists, _I32, t * hk * _list_width(p), "lists"), _flat(counts, _I32, t * hk, "counts"),
-        _ptr(workspace), wb, _word(error))
+        _grid(summary, _BF16, (p.num_pages, hk, 2, 128), "summary"),
+        _flat(cu_q, _I32, seqs + 1, "cu_q"), _flat(kv_lens, _I32, seqs, "kv_lens"),
+        _grid(block_table, _I32, (seqs, p.pages_per_seq), "block_table"),
+        _grid(lists, _I32, (t, hk, _list_width(p)), "lists"),
+        _grid(counts, _I32, (t, hk), "counts"), _ptr(workspace), wb, _word(error))
 
 
 def sparse_paged_attn(params: SpaPagedParams, q, k_cache, v_cache, cu_q, kv_lens, block_table,
@@ -505,9 +536,10 @@ def sparse_paged_attn(params: SpaPagedParams, q, k_cache, v_cache, cu_q, kv_lens
         _lib.sparse_paged_attn, dev, stream, ctypes.byref(p), _rows(q, 1, t, hq, "q"),
         _cache(p, k_cache, "k_cache"), _cache(p, v_cache, "v_cache"),
         _flat(cu_q, _I32, seqs + 1, "cu_q"), _flat(kv_lens, _I32, seqs, "kv_lens"),
-        _flat(block_table, _I32, seqs * p.pages_per_seq, "block_table"),
-        _flat(lists, _I32, t * hk * _list_width(p), "lists"), _flat(counts, _I32, t * hk, "counts"),
-        _rows(o, 1, t, hq, "o"), _flat(lse, _F32, t * hq, "lse"), _ptr(workspace), wb, _word(error))
+        _grid(block_table, _I32, (seqs, p.pages_per_seq), "block_table"),
+        _grid(lists, _I32, (t, hk, _list_width(p)), "lists"),
+        _grid(counts, _I32, (t, hk), "counts"), _rows(o, 1, t, hq, "o"),
+        _grid(lse, _F32, (t, hq), "lse"), _ptr(workspace), wb, _word(error))
 
 
 def sparse_paged_status(error, stream=None) -> int:

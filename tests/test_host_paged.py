@@ -199,6 +199,68 @@ def test_tensor_checks_of_the_binding():
         spa.sparse_paged_status(torch.zeros(1, dtype=torch.int32), stream=0)
 
 
+def test_tensors_of_another_width_are_refused(monkeypatch):
+    """A contiguous tensor with elements enough, but rows of another length, would be read with
+    the wrong row stride.  Accepted ones reach the library, which refuses the head size."""
+    monkeypatch.setattr(binding, "_device", lambda *x: -1)
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+    z = lambda dtype, *shape: torch.zeros(*shape, dtype=dtype)
+    p = paged(head_dim=64, sink_pages=1, local_pages=2, top_pages=3)     # 2 x 4 table, 4 x 2 x 6 lists
+    r = rope(head_dim=64, batch=2)                                       # 64 x 128 table
+    one = paged(head_dim=64, seqs=1, tokens=1, heads_kv=1)
+
+    def on_attn(p, table=A, lists=A, counts=A, lse=A):
+        return spa.sparse_paged_attn(p, ROWS, A, A, A, A, table, lists, counts, ROWS, lse, A, A,
+                                     workspace_bytes=1 << 40, stream=0)
+
+    def on_select(p, table=A, lists=A, counts=A, summary=A):
+        return spa.sparse_paged_select(p, ROWS, summary, A, A, table, lists, counts, A, A,
+                                       workspace_bytes=1 << 40, stream=0)
+
+    def on_append(p, table=A, summary=A, angles=A, weight=None):
+        return spa.sparse_paged_append(p, r, None, ROWS, ROWS, weight, weight, angles, A, A, table,
+                                       None, A, A, summary, A, stream=0)
+
+    def on_rope(r, positions=A, angles=A, weight=None):
+        return spa.sparse_qk_norm_rope(r, ROWS, ROWS, weight, None, positions, angles, ROWS, ROWS, A,
+                                       stream=0)
+
+    for call, kw in ((on_attn, dict(table=z(i32, 2, 5))), (on_attn, dict(table=z(i32, 4, 2))),
+                     (on_attn, dict(table=z(i32, 1, 8))), (on_select, dict(table=z(i32, 2, 5))),
+                     (on_append, dict(table=z(i32, 2, 5))), (on_attn, dict(lists=z(i32, 4, 2, 7))),
+                     (on_select, dict(lists=z(i32, 4, 2, 7))), (on_attn, dict(lists=z(i32, 4, 3, 6))),
+                     (on_attn, dict(counts=z(i32, 4, 3))), (on_select, dict(counts=z(i32, 2, 4))),
+                     (on_attn, dict(lse=z(f32, 4, 8))), (on_attn, dict(lse=z(f32, 3, 4))),
+                     (on_select, dict(summary=z(bf16, 8, 4, 2, 128))),
+                     (on_append, dict(summary=z(bf16, 8, 2, 4, 128))),
+                     (on_append, dict(angles=z(f32, 64, 256))), (on_append, dict(angles=z(f32, 63, 128))),
+                     (on_append, dict(weight=z(bf16, 4, 128))), (on_append, dict(table=z(i32, 7)))):
+        with pytest.raises(ValueError, match="shape|elements"):
+            call(p, **kw)
+    for kw in (dict(positions=z(i32, 2, 5)), dict(angles=z(f32, 128, 64)), dict(weight=z(bf16, 2, 128))):
+        with pytest.raises(ValueError, match="shape"):
+            on_rope(r, **kw)
+    # as wanted, with more rows, flat, or a single row that is longer
+    for call, q, kw in ((on_attn, p, dict(table=z(i32, 2, 4), lists=z(i32, 4, 2, 6),
+                                          counts=z(i32, 4, 2), lse=z(f32, 4, 4))),
+                        (on_attn, p, dict(table=z(i32, 9, 4), lists=z(i32, 5, 2, 6),
+                                          counts=z(i32, 5, 2), lse=z(f32, 6, 4))),
+                        (on_attn, p, dict(table=z(i32, 8), lists=z(i32, 8, 6), counts=z(i32, 20))),
+                        (on_attn, one, dict(table=z(i32, 1, 9), lists=z(i32, 1, 1, 7),
+                                            counts=z(i32, 1, 1), lse=z(f32, 1, 4))),
+                        (on_select, p, dict(summary=z(bf16, 8, 2, 2, 128))),
+                        (on_select, p, dict(summary=z(bf16, 8, 2, 256))),
+                        (on_append, p, dict(angles=z(f32, 80, 128), weight=z(bf16, 128))),
+                        (on_rope, r, dict(positions=z(i32, 2, 4), angles=z(f32, 64, 128),
+                                          weight=z(bf16, 1, 128))),
+                        (on_rope, r, dict(positions=z(i32, 8)))):
+        assert call(q, **kw) == spa.SPA_ERR_UNSUPPORTED
+    with pytest.raises(TypeError):
+        on_attn(p, table=z(torch.int64, 2, 4))
+    with pytest.raises(ValueError, match="contiguous"):
+        on_attn(p, table=z(i32, 2, 8)[:, :4])
+
+
 def test_struct_sizes_match_the_header():
     assert ctypes.sizeof(spa.SpaRows) == 32
     assert ctypes.sizeof(spa.SpaRopeParams) == 36
