@@ -361,3 +361,54 @@ def test_captured_behind_copies_and_joined_streams():
         for x, y in zip(tensors, want):
             assert torch.equal(x, y)
     b.ok()
+
+
+def test_the_stream_given_by_the_caller_is_the_one_used():
+    """Every call's input is filled on that stream alone, behind a delay, so that a call on
+    another stream would read what was there before; results are those of the current stream."""
+    b = Batch(8, 2, 16, [(1, 300), (5, 700), (1, 40)], seed=22)
+    p = b.params(sink_pages=1, local_pages=2, top_pages=5)
+    ws, sm = b.workspace(p), to_gpu(b.summary())
+    r = spa.make_rope_params(1, b.T, 8, 2, table_rows=1024)
+    angles = torch.from_numpy(op.rope_table(1024, D)).cuda()
+    pos = torch.tensor([pos for _, _, pos in b.tokens()], dtype=torch.int32, device="cuda")
+    source, staged, turned = b.q.clone(), torch.zeros_like(b.q), torch.zeros_like(b.q)
+    lens, kv = b.kv_gpu.clone(), torch.zeros_like(b.kv_gpu)
+    kc, vc = torch.zeros_like(b.kc), torch.zeros_like(b.vc)
+    lists = torch.zeros(b.T, 2, 8, dtype=torch.int32, device="cuda")
+    counts = torch.zeros(b.T, 2, dtype=torch.int32, device="cuda")
+    outs = [torch.zeros(b.T, 8, D, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    lses = [torch.zeros(b.T, 8, device="cuda") for _ in range(2)]
+    made = [turned, kc, vc, lists, counts, *outs, *lses]
+
+    def step(stream):
+        spa.check(spa.sparse_qk_norm_rope(r, staged, None, None, None, pos, angles, turned, None,
+                                          b.error, stream=stream))
+        spa.check(spa.sparse_paged_append(p, None, None, b.qkv_gpu[:, 8:10], b.qkv_gpu[:, 10:], None,
+                                          None, None, b.cu_gpu, kv, b.table_gpu, None, kc, vc, None,
+                                          b.error, stream=stream))
+        spa.check(spa.sparse_paged_select(p, turned, sm, b.cu_gpu, kv, b.table_gpu, lists, counts, ws,
+                                          b.error, stream=stream))
+        for i, (x, y) in enumerate(((None, None), (lists, counts))):
+            spa.check(spa.sparse_paged_attn(p, turned, b.kc, b.vc, b.cu_gpu, kv, b.table_gpu, x, y,
+                                            outs[i], lses[i], ws, b.error, stream=stream))
+
+    staged.copy_(source)
+    kv.copy_(lens)
+    step(None)
+    b.ok()
+    want = [x.clone() for x in made]
+    s = torch.cuda.Stream()
+    for given in (s, s.cuda_stream):
+        for x in [staged, kv, *made]:
+            x.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)          # some ten milliseconds
+            staged.copy_(source)
+            kv.copy_(lens)
+        step(given)
+        s.synchronize()
+        for x, y in zip(made, want):
+            assert torch.equal(x, y)
+        spa.check(spa.sparse_paged_status(b.error, stream=given))
