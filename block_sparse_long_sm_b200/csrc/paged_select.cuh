@@ -45,10 +45,14 @@
 //                    order.  Bound by latency, the barriers and the loads between:
 //                    8.4 us for one token among 2042 pages, 9.9 us for 16 (with a
 //                    radix search there: 14 and 17 us).
-// page_top_warp_kernel  the same by one warp, for up to 512 candidates: no barriers,
-//                    and all of a chunk's tokens are under way at once: 20 us for
-//                    2000 selections among 506 pages, the whole step 211 us (218 us
-//                    with a block each).
+//                    Radix search above 2048 candidates: scores and ranking for one
+//                    token 15.9 us at 2054 candidates (11.0 us at 2048 with the points,
+//                    14.6 us with a radix search), 22 us at 4090, 37 us at 8186.
+// page_top_warp_kernel  the same by one warp, for up to 512 candidates and many
+//                    selections: no barriers, and all of a chunk's tokens are under
+//                    way at once: 20 us for 2000 selections among 506 pages.  A warp
+//                    alone takes longer over its keys than a block does, so few
+//                    selections are left to blocks.
 #pragma once
 
 #include "paged_seqs.cuh"
@@ -659,6 +663,15 @@ __device__ __forceinline__ uint32_t bit_rank(uint32_t v, int bit, uint32_t rank,
 
 constexpr int kTopWarpThreads = 128;
 constexpr int kTopWarpKeys = 512;
+// Fewer selections (tokens x kv heads) than about seven per SM go to blocks.  Scores
+// and ranking in us, by warps / by blocks, among 128, 256 and 512 candidates:
+//     8 selections     12.1 /  9.4    14.9 /  9.9    19.6 / 10.6
+//   128 (16 tokens)    14.6 / 10.7    17.4 / 11.7    25.1 / 16.0
+//   640 (80 tokens)    21.4 / 20.9    33.0 / 29.5    65.5 / 58.1
+//  1024 (two chunks)   17.1 / 20.0    23.2 / 24.8    32.8 / 31.0
+//  1536 (two chunks)   18.6 / 25.8    25.5 / 32.0    39.6 / 41.9
+//  2000 (two chunks)   22.2 / 33.6    30.8 / 39.9    45.9 / 52.2
+constexpr int kTopWarpSelections = 1024;
 
 struct TopWarpSmem {
   uint32_t keys[kTopWarpKeys];

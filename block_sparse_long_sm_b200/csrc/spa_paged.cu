@@ -364,7 +364,7 @@ SPA_API spa_status sparse_paged_select(const spa_paged_params* p, const spa_rows
   }
   // (begins while the scores are computed: it reads the lengths meanwhile)
   bool ok;
-  if (most > kTopWarpKeys) {
+  if (most > kTopWarpKeys || tg < kTopWarpSelections) {
     static_assert(top_smem_bytes(INT_MAX) <= kSpreadMax, "one limit for both");
     if (set_smem(page_top_kernel, kSpreadMax) != cudaSuccess) return SPA_ERR_CUDA;
     ok = launch_after(scored, page_top_kernel, dim3((unsigned)tg), kTopThreads,

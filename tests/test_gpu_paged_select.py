@@ -178,3 +178,39 @@ def test_more_rankings_than_sms():
     o, lse = attend(b, p, lists, counts, ws=ws)
     check_attention(b, o, lse, pages_of=lambda t, g: want[(t, g)], rows={0, 11, 12, 41})
     b.ok()
+
+
+@pytest.mark.parametrize("tokens", [127, 128, 131])
+@pytest.mark.parametrize("pages,tops,kinds", [(40, (1, 30), 90), (135, (1, 26, 131), 600),
+                                              (515, (1, 100, 511), 700), (515, (73, 257), 5),
+                                              (200, (28, 100), 1), (516, (100,), 700)])
+def test_many_selections_at_once(tokens, pages, tops, kinds):
+    """Around a thousand tokens x kv heads, where whole warps take over from blocks, over tables
+    that share physical pages (few kinds of them: many equal scores)."""
+    hq, hkv, page = 16, 8, 16
+    b = Batch(hq, hkv, page, [(1, 1)] * tokens, seed=tokens, free=max(0, kinds - tokens), extra_cols=0,
+              pad_rows=1)
+    rng = np.random.default_rng(pages + kinds)
+    b.per_seq = pages
+    b.table = rng.integers(0, min(kinds, b.num_pages), size=(tokens, pages)).astype(np.int32)
+    b.table_gpu = torch.from_numpy(b.table).cuda()
+    b.kv = [int(x) for x in rng.integers(1, pages * page + 1, size=tokens)]
+    b.kv[0], b.kv[1], b.kv[-1] = pages * page, 3, pages * page - 7
+    b.kv_gpu = torch.tensor(b.kv, dtype=torch.int32).cuda()
+    raw = rng.standard_normal((b.num_pages, hkv, 2, D))
+    sm = bits_of(np.stack([raw.min(2), raw.max(2)], 2))
+    pick = [0, 1, 2, tokens // 2, tokens - 1]
+    for top in tops:
+        _, _, lists, counts, _ = run_select(b, 1, 2, top, summary=sm)
+        lh, ch = lists.cpu().numpy(), counts.cpu().numpy()
+        for t in pick:
+            for g in (0, 5, hkv - 1):
+                q = f64(b.qkv[t, 2 * g:2 * g + 2])
+                smf = f64(sm[:, g])
+                u = op.page_bounds(q, smf[:, 0], smf[:, 1])
+                want = op.select_pages(b.kv[t] - 1, page, 1, 2, top, lambda a, z: u[b.table[t, a:z]])
+                assert ch[t, g] == want.size
+                assert np.array_equal(lh[t, g, :want.size], want), (t, g)
+                assert np.all(lh[t, g, want.size:] == -1)
+        assert np.all(lh[tokens] == -7) and np.all(ch[tokens] == -7)
+    b.ok()
