@@ -45,10 +45,12 @@ __device__ __forceinline__ int append_segments(const Seqs& v, int s) {
   return ((q.kv - 1) >> v.shift) - ((q.kv - q.n) >> v.shift) + 1;
 }
 
-// Five blocks per SM (102 registers): the 760 blocks of five ragged chunks, 7300
-// tokens of 8 kv heads, run in about one round, 14.0 us (3.4 TB/s; four blocks
-// 19.7 us, six 17.7 us); one token each of 64 sequences takes 5.6 us.  Bound by
-// the way of a block: lengths, table, rows, summary.
+// Five blocks per SM (96 registers, 8 bytes spilled): the 760 blocks of
+// five ragged chunks, 7300 tokens of 8 kv heads, run in about one round, 14.0 us
+// (3.4 TB/s; four blocks 19.7 us, six 17.7 us); one token each of 64 sequences
+// takes 5.6 us.  Held off the memory's rate by the latency of a block's way, each
+// step after the one before: lengths, table, its rows 16 at a time, the rows that
+// the page held, summary.
 __global__ void __launch_bounds__(kAppendThreads, 5) paged_append_kernel(const AppendArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the attention waits by itself
   const int lane = threadIdx.x & 31, li = lane & 7, warp = threadIdx.x >> 5;

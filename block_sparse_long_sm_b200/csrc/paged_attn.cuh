@@ -49,7 +49,10 @@
 // Roles (384 threads): warps 0-3 / 4-7 softmax of slot 0 / 1, warp 8 loads,
 // warp 9 MMA, TMEM and the ends of V tiles, warp 10 walks the CTA's piece and
 // hands its segments to the others through a ring of four, so that the lengths,
-// lists and page numbers of the next units are read ahead.
+// lists and page numbers of the next units are read ahead.  Launched with 168
+// registers a thread (the compiler spills 176 bytes, 168 with lists), split into
+// 56 and 224.  tests/paged_protocol.py plays the roles on the CPU: who waits for
+// what, and who may still read what another writes.
 //
 // Measured (one B200; bound): 2048 tokens at 32K, 32/8 heads, 1.04-1.12 ms, 950
 // to 1026 TFLOP/s (the way of a tile's scores through its warpgroup: tensor

@@ -35,8 +35,10 @@
 //                    terms is free, so the pieces are the matrix operand as
 //                    they come).  Tokens of one sequence that fit into the
 //                    sixteen rows share the loads.  16 sequences of up to 32K in
-//                    pages of 16: 50 MB of summaries, 22 us (2.3 TB/s); 250 tokens
-//                    that share 6 MB: 32 us (loads from L2, three products a page).
+//                    pages of 16: 50 MB of summaries, 22 us (2.3 TB/s: three blocks
+//                    per SM of 168 registers, 32 bytes spilled, have few loads under
+//                    way); 250 tokens that share 6 MB: 32 us (loads from L2, three
+//                    products a page).
 // page_top_kernel    one block per token and kv head: the score of rank top_pages
 //                    is found to within the error of the sums, by counting keys
 //                    above three points of an interval (up to 2048 candidates,

@@ -333,7 +333,7 @@ SPA_API spa_status sparse_key_mass(const spa_params* p, const void* q, const voi
  *
  * Sequences.  S sequences bring n_s = cu_q[s+1] - cu_q[s] new tokens each
  * (rows cu_q[s] .. cu_q[s+1] of q, k, v, o; n_s may be 0, and rows outside
- * [cu_q[0], cu_q[S]) are neither read nor written).  kv_lens[s] is the length
+ * [cu_q[0], cu_q[S]) are not written and may hold anything).  kv_lens[s] is the length
  * of sequence s with its new tokens, so token i of it has position
  * kv_lens[s] - n_s + i.  Position x lies in page block_table[s][x / page_size],
  * row x % page_size.
