@@ -373,15 +373,17 @@ def _grid(x, dtype, shape, name):
         return x
     if x.shape == shape and x.dtype is dtype and x.is_contiguous():
         return x.data_ptr()
-    dim, count = x.dim(), math.prod(shape)
-    if dim == len(shape):
+    given, count = tuple(x.shape), math.prod(shape)
+    while len(given) > len(shape) and given[0] == 1:
+        given = given[1:]
+    if len(given) == len(shape):
         # a dimension's length is a stride unless there is only one row of it
         rows, good = 1, True
-        for have, want in zip(x.shape, shape):
+        for have, want in zip(given, shape):
             good = good and (have == want or (have > want and rows <= 1))
             rows *= want
     else:
-        good = dim == 1 or x.numel() == count
+        good = len(given) == 1 or x.numel() == count
     if not good:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted {shape}")
     return _flat(x, dtype, count, name)

@@ -251,6 +251,7 @@ def test_tensors_of_another_width_are_refused(monkeypatch):
                         (on_select, p, dict(summary=z(bf16, 8, 2, 2, 128))),
                         (on_select, p, dict(summary=z(bf16, 8, 2, 256))),
                         (on_append, p, dict(angles=z(f32, 80, 128), weight=z(bf16, 128))),
+                        (on_append, p, dict(angles=z(f32, 1, 80, 128), table=z(i32, 1, 3, 4))),
                         (on_rope, r, dict(positions=z(i32, 2, 4), angles=z(f32, 64, 128),
                                           weight=z(bf16, 1, 128))),
                         (on_rope, r, dict(positions=z(i32, 8)))):
